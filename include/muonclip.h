@@ -18,6 +18,14 @@
  *   mc_polar_express_coeffs  host: a Polar Express coefficient table for mc_hparams
  *   mc_shard_plan            host: whole-matrix ownership for a sharded step
  *
+ * and the activation operators that make the step's inputs (last section):
+ *
+ *   mc_rms_norm, mc_rms_norm_backward      norm with the residual's addition, 8-bit output
+ *   mc_act8_pack, mc_act8_unpack           activations kept in 8 bits
+ *   mc_weight_grad, mc_expert_weight_grad  gradients of one or of every expert's weight
+ *   mc_expert_sort, mc_expert_gather, mc_expert_combine, mc_expert_combine_backward
+ *                                          tokens sorted by expert and back
+ *
  * Conventions for every call
  *   - All pointers named "device" are CUDA device pointers on the current
  *     device; they must be 16-byte aligned.  The library never frees or
@@ -461,11 +469,155 @@ typedef struct {
 int mc_profile_begin(void);
 int mc_profile_end(mc_kernel_stat* out, int max_rows, int* rows);
 
+/* ========================================================================
+ * Activation operators: what a training step does around the optimizer step to
+ * produce its inputs, the layer inputs x (mc_qk_max_logit, mc_mla_max_logit) and
+ * the weight gradients (mc_param.g).  The conventions above hold.  Row counts
+ * are at most 2^31 - 1, columns at most 2^24.  Matrices are contiguous except
+ * where a structure gives row strides.
+ * ======================================================================== */
+
+/* An activation in 8 bits: rows x cols values in blocks of 32 consecutive
+ * columns of a row (the last block of a row may be shorter).  Block b of row r
+ * has the scale byte s = scale[r * s_ld + b], column c the code q[r * q_ld + c];
+ * the value is code * 2^(s - 127), code an e4m3 number (MC_ACT_E4M3: 4 bits of
+ * exponent, 3 of fraction, largest 448) or a two's complement int8
+ * (MC_ACT_INT8).  s = 255: the whole block is NaN.  Writers choose the least
+ * k >= -120 with max|x| <= 448 * 2^k (127 * 2^k), s = k + 127, and the nearest code to
+ * x * 2^-k, ties to even (|x| up to half a step below 2^128 stays finite); a block
+ * that holds a NaN or an infinity gets s = 255 and zero codes.  Every value
+ * written so is exact in bf16.  Bytes between cols and q_ld, and behind the last
+ * scale of a row, are neither written nor used. */
+enum { MC_ACT_E4M3 = 16, MC_ACT_INT8 = 17 };
+typedef struct {
+  void* q;          /* device, rows x q_ld bytes, 16-byte aligned */
+  void* scale;      /* device, rows x s_ld bytes, 16-byte aligned */
+  int64_t rows;     /* >= 0 */
+  int64_t cols;     /* >= 1 */
+  int64_t q_ld;     /* multiple of 16, >= cols */
+  int64_t s_ld;     /* multiple of 16, >= ceil(cols / 32) */
+  int32_t fmt;      /* MC_ACT_E4M3 or MC_ACT_INT8 */
+  int32_t reserved;
+} mc_act8;
+
+/*
+ * mc_act8_pack -- x (device, rows x cols, MC_F32 or MC_BF16) to 8 bits.
+ * mc_act8_unpack -- its values to out (device, rows x cols, MC_F32 or MC_BF16).
+ * The operands must not overlap.  rows == 0 is a no-op.
+ */
+int mc_act8_pack(const void* x, int x_dtype, const mc_act8* a, void* stream);
+int mc_act8_unpack(const mc_act8* a, void* out, int out_dtype, void* stream);
+
+/*
+ * mc_rms_norm -- root-mean-square norm with the residual's addition:
+ *   h = x + residual, rounded to dtype and stored in h_out (residual and h_out
+ *       both NULL: h = x);  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * w
+ * in fp32 from the stored h.  y goes to y_out (bf16) or, unrounded, to the 8-bit
+ * y8: exactly one of them is given.  h_out may be x or residual itself; nothing
+ * else may overlap.
+ * x, residual, h_out  device, rows x cols, dtype (MC_F32 or MC_BF16)
+ * w                   device, cols, w_dtype
+ * rstd_out            device fp32 [rows]
+ * cols                at most 32768; eps >= 0.  rows == 0 is a no-op.
+ */
+int mc_rms_norm(const void* x, const void* residual, const void* w, int dtype, int w_dtype, int64_t rows, int64_t cols,
+                float eps, void* h_out, void* y_out, const mc_act8* y8, float* rstd_out, void* stream);
+
+/*
+ * mc_rms_norm_backward -- its gradient.  With xhat = h * rstd and g = dy * w:
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dh      (the gradient of x and of residual)
+ *   dw = sum over rows of dy * xhat                    (fp32 [cols])
+ * h      the stored h (dtype), or NULL with h8 its 8-bit form
+ * dh     gradient that reaches h past the norm (dtype), or NULL for none
+ * dx     dtype; may be dy or dh itself
+ * The row sums and dw are added in a fixed order.  rows == 0 gives dw = 0.
+ * workspace  >= mc_rms_norm_backward_workspace_size(rows, cols) bytes, or NULL.
+ */
+size_t mc_rms_norm_backward_workspace_size(int64_t rows, int64_t cols);
+int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, const mc_act8* h8, const void* w,
+                         const float* rstd, int dtype, int w_dtype, int64_t rows, int64_t cols, void* dx, float* dw,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mc_weight_grad -- the gradient of an nn.Linear weight (rows = out-features)
+ * from its output's gradient and its input kept in 8 bits:
+ *   g[m][n] = sum over rows r of dy[r][m] * x[r][n]        (accumulate: added to g)
+ * on tensor cores, with x's values exact in bf16 and fp32 accumulation; an fp32
+ * sum is carried over at most 4096 rows inside the tensor cores, then in fp32
+ * registers of the memory system or in ranges joined in order.  Results do not
+ * depend on anything but the operands and their sizes.
+ * dy     device bf16, x->rows x out_features
+ * g      device, out_features x x->cols, g_dtype; accumulate needs MC_F32
+ * x->rows == 0 gives g = 0 (accumulate: unchanged).
+ * workspace  >= mc_weight_grad_workspace_size(x->rows, out_features, x->cols), or NULL.
+ */
+size_t mc_weight_grad_workspace_size(int64_t rows, int64_t out_features, int64_t in_features);
+int mc_weight_grad(const void* dy, const mc_act8* x, int64_t out_features, void* g, int g_dtype, int accumulate,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mc_expert_weight_grad -- mc_weight_grad of every expert's weight in one call:
+ *   g[e][m][n] = sum over rows r in [offsets[e], offsets[e + 1]) of dy[r][m] * x[row(r)][n]
+ * dy       device bf16, rows x out_features, rows sorted by expert (mc_expert_sort)
+ * x        row(r) = r (source NULL: x has `rows` rows, sorted like dy), or
+ *          row(r) = source[r] / top_k (x has rows / top_k rows, in token order; an
+ *          entry that names none of them counts as a row of zeros)
+ * offsets  device int32 [experts + 1]; taken into [0, rows] where they are not
+ * g        device, experts x out_features x x->cols, g_dtype; accumulate needs MC_F32.
+ *          An expert without rows gets zeros (accumulate: is left as it is).
+ * Rows of dy outside every expert are not read into any result, whatever they hold.
+ * experts, top_k  at most 1024
+ * workspace  >= mc_expert_weight_grad_workspace_size(...), or NULL.
+ */
+size_t mc_expert_weight_grad_workspace_size(int64_t rows, int experts, int64_t out_features, int64_t in_features);
+int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int32_t* offsets, const int32_t* source,
+                          int top_k, int experts, int64_t out_features, void* g, int g_dtype, int accumulate,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mc_expert_sort -- the order of `tokens` tokens' top_k pairs by expert, stable.
+ * idx       device int32 or int64 (idx_bits 32 or 64) [tokens][top_k]: the expert
+ *           of each pair; a pair whose index is outside [0, experts) is dropped
+ * offsets   device int32 [experts + 1]: first sorted row of each expert; the last
+ *           entry is the number of rows
+ * source    device int32 [tokens * top_k]: the pair t * top_k + k of each sorted
+ *           row, -1 behind the last row
+ * position  device int32 [tokens][top_k]: the row of each pair, -1 if dropped
+ * experts, top_k  at most 1024; tokens * top_k below 2^31.  tokens == 0: offsets = 0.
+ * workspace  >= mc_expert_sort_workspace_size(...), or NULL.
+ */
+size_t mc_expert_sort_workspace_size(int64_t tokens, int top_k, int experts);
+int mc_expert_sort(const void* idx, int idx_bits, int64_t tokens, int top_k, int experts, int32_t* offsets,
+                   int32_t* source, int32_t* position, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mc_expert_gather -- rows_out[position[t][k]] = x[t]  (x [tokens][cols], rows_out
+ * [tokens * top_k][cols], dtype).  Rows that no pair has are left as they are.
+ *
+ * mc_expert_combine -- out[t] = sum over k of weights[t][k] * y[position[t][k]], k
+ * ascending in fp32, rounded once; dropped pairs add nothing, a token without
+ * pairs gets zeros.  weights: device fp32 [tokens][top_k], or NULL for ones (the
+ * gradient of mc_expert_gather).
+ *
+ * mc_expert_combine_backward -- dy[position[t][k]] = weights[t][k] * dout[t] and
+ * dweights[t][k] = <dout[t], y[position[t][k]]> (fp32; 0 for a dropped pair).  Rows of
+ * dy that no pair has are left as they are.  dy may be y itself.
+ *
+ * position is mc_expert_sort's; an entry outside [0, tokens * top_k) counts as dropped.
+ * tokens == 0 is a no-op.
+ */
+int mc_expert_gather(const void* x, int dtype, int64_t tokens, int top_k, int64_t cols, const int32_t* position,
+                     void* rows_out, void* stream);
+int mc_expert_combine(const void* y, int dtype, int64_t tokens, int top_k, int64_t cols, const int32_t* position,
+                      const float* weights, void* out, void* stream);
+int mc_expert_combine_backward(const void* dout, const void* y, int dtype, int64_t tokens, int top_k, int64_t cols,
+                               const int32_t* position, const float* weights, void* dy, float* dweights, void* stream);
+
 /*
  * mc_struct_size -- host-only: sizeof of this header's structures as the
  * library was built, for bindings that lay the structures out themselves:
- * 0 mc_param, 1 mc_hparams, 2 mc_normuon, 3 mc_clip_slice, 4 mc_kernel_stat;
- * 0 for any other index.
+ * 0 mc_param, 1 mc_hparams, 2 mc_normuon, 3 mc_clip_slice, 4 mc_kernel_stat,
+ * 16 mc_act8; 0 for any other index.
  */
 size_t mc_struct_size(int which);
 

@@ -8,8 +8,10 @@ missing or the device is not a B200 the calls raise.
     from matrix_orthogonalising_optimizer_step_b200 import muon_step, qk_max_logit, qk_clip
 
 Also: muon_step_host_grads, normuon_step, mla_max_logit, qk_clip_slices (with
-mla_slices), polar_express_coeffs, shard_plan, qk_max_logit_static, and the
-data-parallel step in ``sharded``.
+mla_slices), polar_express_coeffs, shard_plan, qk_max_logit_static, the
+data-parallel step in ``sharded``, and the operators of ``activations`` that
+make the step's inputs (norm, 8-bit activations, weight gradients, tokens by
+expert).
 """
 from __future__ import annotations
 
@@ -30,7 +32,12 @@ EXPORTS = ("mc_muon_workspace_size", "mc_muon_step", "mc_qk_workspace_size", "mc
            "mc_qk_max_logit_static", "mc_qk_clip_slices", "mc_mla_workspace_size", "mc_mla_max_logit",
            "mc_shard_plan", "mc_normuon_workspace_size", "mc_normuon_step", "mc_polar_express_coeffs",
            "mc_muon_host_grads_workspace_size", "mc_muon_step_host_grads", "mc_selftest_bounded_wait",
-           "mc_struct_size")
+           "mc_struct_size",
+           "mc_act8_pack", "mc_act8_unpack", "mc_rms_norm", "mc_rms_norm_backward_workspace_size",
+           "mc_rms_norm_backward", "mc_weight_grad_workspace_size", "mc_weight_grad",
+           "mc_expert_weight_grad_workspace_size", "mc_expert_weight_grad", "mc_expert_sort_workspace_size",
+           "mc_expert_sort", "mc_expert_gather", "mc_expert_combine", "mc_expert_combine_backward")
+MC_ACT_E4M3, MC_ACT_INT8 = 16, 17
 MC_QK_STATIC_MAX_ELEMS = 1 << 24
 MC_QK_STATIC_MAX_HEADS = 4096
 
@@ -63,6 +70,12 @@ class McKernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32), ("total_ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("flops_executed", ctypes.c_double),
                 ("flops_dense_equiv", ctypes.c_double), ("bytes", ctypes.c_double)]
+
+
+class McAct8(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("q_ld", ctypes.c_int64), ("s_ld", ctypes.c_int64),
+                ("fmt", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MuonClipError(RuntimeError):
@@ -128,6 +141,24 @@ def load_library():
     lib.mc_profile_begin.restype = i32
     lib.mc_profile_end.argtypes = [P(McKernelStat), i32, P(ctypes.c_int)]
     lib.mc_profile_end.restype = i32
+    i64, act8 = ctypes.c_int64, P(McAct8)
+    for name, args, res in (
+            ("mc_act8_pack", [vp, i32, act8, vp], i32),
+            ("mc_act8_unpack", [act8, vp, i32, vp], i32),
+            ("mc_rms_norm", [vp, vp, vp, i32, i32, i64, i64, ctypes.c_float, vp, vp, act8, vp, vp], i32),
+            ("mc_rms_norm_backward_workspace_size", [i64, i64], sz),
+            ("mc_rms_norm_backward", [vp, vp, vp, act8, vp, vp, i32, i32, i64, i64, vp, vp, vp, sz, vp], i32),
+            ("mc_weight_grad_workspace_size", [i64, i64, i64], sz),
+            ("mc_weight_grad", [vp, act8, i64, vp, i32, i32, vp, sz, vp], i32),
+            ("mc_expert_weight_grad_workspace_size", [i64, i32, i64, i64], sz),
+            ("mc_expert_weight_grad", [vp, i64, act8, vp, vp, i32, i32, i64, vp, i32, i32, vp, sz, vp], i32),
+            ("mc_expert_sort_workspace_size", [i64, i32, i32], sz),
+            ("mc_expert_sort", [vp, i32, i64, i32, i32, vp, vp, vp, vp, sz, vp], i32),
+            ("mc_expert_gather", [vp, i32, i64, i32, i64, vp, vp, vp], i32),
+            ("mc_expert_combine", [vp, i32, i64, i32, i64, vp, vp, vp, vp], i32),
+            ("mc_expert_combine_backward", [vp, vp, i32, i64, i32, i64, vp, vp, vp, vp, vp], i32)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
     _lib = lib
     return lib
 
@@ -413,15 +444,26 @@ def normuon_step(weights: Sequence, grads: Sequence, moms: Sequence, vs: Sequenc
                                    int(ws.numel() * ws.element_size()), _ptr(norms_out), _stream_handle(stream)))
 
 
+def _layer_input(x, stream):
+    """A layer input kept in 8 bits (Act8) as the bf16 tensor it stands for
+    (exactly, if act8_pack or rms_norm wrote it); a tensor is returned as it is."""
+    if hasattr(x, "fmt") and hasattr(x, "scale"):
+        from .activations import act8_unpack
+        return act8_unpack(x, stream=stream)
+    return x
+
+
 def qk_workspace_size(B, S, D, H, dh) -> int:
     return int(load_library().mc_qk_workspace_size(B, S, D, H, dh))
 
 
 def qk_max_logit(x, wq, wk, H: int, dh: int, *, causal: bool = True, smax_out=None,
                  workspace=None, stream=None):
-    """Per-head S_max (fp32 [H]) of causal attention with Q = x Wq^T, K = x Wk^T."""
+    """Per-head S_max (fp32 [H]) of causal attention with Q = x Wq^T, K = x Wk^T.
+    x: bf16 [B, S, D], or an Act8 of that shape."""
     torch = _torch()
     lib = load_library()
+    x = _layer_input(x, stream)
     _check_qk_args(x, wq, wk, H, dh, smax_out)
     dev = _one_device([x, wq, wk, smax_out, workspace])
     B, S, D = x.shape
@@ -518,9 +560,11 @@ def mla_max_logit(x, wqc, wkc, wqr, wkr, H: int, dc: int, dr: int, *, causal: bo
                   workspace=None, stream=None):
     """Per-head S_max (fp32 [H]) of multi-head latent attention: content part
     x W_qC^T . x W_kC^T per head plus rotary part x W_qR^T . x W_kR^T with one
-    shared rotary key, over sqrt(dc + dr) (see mc_mla_max_logit)."""
+    shared rotary key, over sqrt(dc + dr) (see mc_mla_max_logit).  x: bf16
+    [B, S, D], or an Act8 of that shape."""
     torch = _torch()
     lib = load_library()
+    x = _layer_input(x, stream)
     for t, nm in ((x, "x"), (wqc, "wqc"), (wkc, "wkc"), (wqr, "wqr"), (wkr, "wkr")):
         _need_cuda_contig(t, nm)
         if t.dtype != torch.bfloat16:
@@ -580,6 +624,8 @@ def qk_max_logit_static(x, wq, wk, H: int, dh: int, *, causal: bool = True, smax
     pass it in to keep the whole call allocation-free.)"""
     torch = _torch()
     lib = load_library()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a bfloat16 tensor (an Act8 needs memory for its values: unpack it, or use qk_max_logit)")
     _check_qk_args(x, wq, wk, H, dh, smax_out)
     dev = _one_device([x, wq, wk, smax_out])
     B, S, D = x.shape
@@ -589,3 +635,19 @@ def qk_max_logit_static(x, wq, wk, H: int, dh: int, *, causal: bool = True, smax
         _check(lib.mc_qk_max_logit_static(_ptr(x), _ptr(wq), _ptr(wk), B, S, D, H, dh, int(causal),
                                           _ptr(smax_out), _stream_handle(stream)))
     return smax_out
+
+
+# ------------------------------------------------------ activation operators
+_ACTIVATIONS = ("Act8", "ExpertPlan", "RmsNorm", "act8_empty", "act8_pack", "act8_unpack", "rms_norm",
+                "rms_norm_backward", "weight_grad", "expert_sort", "expert_gather", "expert_combine",
+                "expert_combine_backward", "expert_weight_grad")
+
+
+def __getattr__(name):
+    """The operators of ``activations`` under the package's own name, loaded on
+    first use (that module needs torch; this one loads without it)."""
+    if name in _ACTIVATIONS:
+        from . import activations
+        globals().update({n: getattr(activations, n) for n in _ACTIVATIONS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -18,14 +18,16 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuonclip.so")
-SOURCES = ["muonclip.cu"]
-HEADERS = ["ptx.cuh", "umma_gemm.cuh", "stream_kernels.cuh", "thin_ns.cuh", "qk_rowmax.cuh"]
+SOURCES = ["muonclip.cu", "activations.cu"]
+HEADERS = ["host.h", "ptx.cuh", "umma_gemm.cuh", "stream_kernels.cuh", "thin_ns.cuh", "qk_rowmax.cuh", "act8.cuh",
+           "norm.cuh", "weight_grad.cuh", "experts.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "-shared", "--cudart", "static",
+    "--threads", "2",          # the two sources side by side
 ]
 
 

@@ -25,6 +25,7 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "muonclip.h"
 #include "ptx.cuh"
 #include "qk_rowmax.cuh"
@@ -32,11 +33,13 @@
 #include "thin_ns.cuh"
 #include "umma_gemm.cuh"
 
-#define MC_API extern "C" __attribute__((visibility("default")))
-
 namespace mc {
 __device__ int g_device_error = 0;
-}
+
+std::mutex g_mu;
+thread_local bool t_prof = false;
+thread_local std::vector<ProfRec> t_recs;
+}  // namespace mc
 
 namespace {
 
@@ -44,47 +47,11 @@ using namespace mc;
 
 thread_local std::string t_last_error;
 
-int fail(int code, const std::string& msg) {
-  t_last_error = msg;
-  return code;
-}
-
-#define MC_CUDA(expr)                                                                      \
-  do {                                                                                     \
-    cudaError_t e_ = (expr);                                                               \
-    if (e_ != cudaSuccess) return fail(MC_ERR_CUDA, std::string(#expr) + ": " + cudaGetErrorString(e_)); \
-  } while (0)
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Largest dynamic shared memory a CTA may opt into on sm_100.
-constexpr int kSmemOptIn = 232448;
 // Newton-Schulz iterations that take a*X from the iterate's hi + lo halves.
 constexpr int kMixedIters = 2;
 
-struct DeviceState {
-  bool init = false;
-  int sms = 0;
-  int pair_clusters = 0;  // CTA pairs of the GEMM kernel that fit on the device at once
-  int cc_major = 0, cc_minor = 0;
-  int* err_ptr = nullptr;
-  void* own_ws = nullptr;
-  size_t own_ws_bytes = 0;
-  // mc_muon_step_host_grads: a non-blocking stream for the gradient copies and
-  // events that order each chunk's compute after its copies
-  cudaStream_t copy_stream = nullptr;
-  std::vector<cudaEvent_t> chunk_ev;
-};
-
-std::mutex g_mu;
 std::map<int, DeviceState> g_devices;
 EncodeTiledFn g_encode = nullptr;
-
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-inline int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <int EPI, int WIDE>
 cudaError_t set_gemm_attr() {
@@ -92,8 +59,14 @@ cudaError_t set_gemm_attr() {
                               static_cast<int>(gemm_smem_bytes<EPI, WIDE>()));
 }
 
-// Caller holds g_mu.
-int device_state(DeviceState** out) {
+}  // namespace
+
+int mc::fail(int code, const std::string& msg) {
+  t_last_error = msg;
+  return code;
+}
+
+int mc::device_state(DeviceState** out) {
   int dev = 0;
   MC_CUDA(cudaGetDevice(&dev));
   DeviceState& st = g_devices[dev];
@@ -150,49 +123,16 @@ int device_state(DeviceState** out) {
   return MC_OK;
 }
 
-// ----------------------------------------------------------- profiling
-enum Kind : int { K_MOMENTUM, K_FINALIZE, K_GRAM, K_POLY, K_APPLY_MIXED, K_APPLY, K_APPLY_FINAL, K_QK_PROJ,
-                  K_QK_CMAX, K_QK_KEYS, K_QK_CLIP, K_MLA_PROJ, K_MLA_CMAX, K_QK_CLIP_SLICES, K_NORM_ROWS,
-                  K_NORM_APPLY, K_TABLE_UPLOAD, K_NS_THIN, K_COUNT };
+namespace {
+
 const char* const kKindNames[K_COUNT] = {"momentum",  "norm_finalize",  "ns_gram", "ns_poly",
                                          "ns_apply_mixed", "ns_apply", "ns_apply_final", "qk_proj",
                                          "qk_causal_max", "qk_keys", "qk_clip", "mla_proj",
                                          "mla_causal_max", "qk_clip_slices", "normuon_rows",
-                                         "normuon_apply", "table_upload", "ns_thin"};
-struct ProfRec {
-  int kind;
-  cudaEvent_t b, e;
-  double flops, flops_exec, flops_dense, bytes;
-};
-thread_local bool t_prof = false;
-thread_local std::vector<ProfRec> t_recs;
-
-// Brackets one launch with CUDA events on its stream while profiling is on.
-struct ProfScope {
-  bool on = false;
-  ProfRec r{};
-  cudaStream_t s;
-  ProfScope(int kind, cudaStream_t st, double flops = 0, double flops_exec = 0, double bytes = 0,
-            double flops_dense = -1) : s(st) {
-    if (!t_prof || kind < 0) return;
-    r.kind = kind;
-    r.flops = flops;
-    r.flops_exec = flops_exec;
-    r.flops_dense = flops_dense < 0 ? flops : flops_dense;
-    r.bytes = bytes;
-    if (cudaEventCreate(&r.b) != cudaSuccess) return;
-    if (cudaEventCreate(&r.e) != cudaSuccess) {
-      cudaEventDestroy(r.b);
-      return;
-    }
-    on = cudaEventRecord(r.b, s) == cudaSuccess;
-  }
-  ~ProfScope() {
-    if (!on) return;
-    cudaEventRecord(r.e, s);
-    t_recs.push_back(r);
-  }
-};
+                                         "normuon_apply", "table_upload", "ns_thin", "act8_pack", "act8_unpack",
+                                         "rms_norm", "rms_norm_backward", "rms_norm_dw", "weight_grad_prepare",
+                                         "weight_grad", "weight_grad_join", "expert_sort", "expert_gather",
+                                         "expert_combine", "expert_combine_backward"};
 
 // One launch of table_fill_kernel<BYTES> with `n` bytes (n <= BYTES).
 template <unsigned BYTES>
@@ -226,7 +166,9 @@ int upload(const void* host, size_t bytes, void* dst, cudaStream_t s) {
   return MC_OK;
 }
 
-int own_workspace(DeviceState& st, size_t bytes, void** ws) {
+}  // namespace
+
+int mc::own_workspace(DeviceState& st, size_t bytes, void** ws) {
   if (st.own_ws_bytes < bytes) {
     if (st.own_ws) {
       MC_CUDA(cudaDeviceSynchronize());
@@ -241,9 +183,9 @@ int own_workspace(DeviceState& st, size_t bytes, void** ws) {
   return MC_OK;
 }
 
-// bf16 tensor map (128-byte swizzle unless given), zero fill out of bounds.
-int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-             const uint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+int mc::make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                 const uint32_t* box, CUtensorMapSwizzle swizzle,
+                 CUtensorMapDataType type) {
   cuuint64_t gd[5], gs[4];
   cuuint32_t bx[5], es[5];
   for (int i = 0; i < rank; ++i) {
@@ -252,12 +194,14 @@ int make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
     es[i] = 1;
   }
   for (int i = 0; i + 1 < rank; ++i) gs[i] = strides[i];
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), gd, gs, bx, es,
+  const CUresult r = g_encode(map, type, rank, const_cast<void*>(base), gd, gs, bx, es,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MC_ERR_CUDA, "cuTensorMapEncodeTiled failed with code " + std::to_string(r));
   return MC_OK;
 }
+
+namespace {
 
 // [count][rows][ld] bf16, box {box_cols, box_rows, 1}
 int map_batched(CUtensorMap* map, const void* base, int64_t count, int64_t rows, int64_t cols, int64_t ld,
@@ -291,8 +235,8 @@ double gemm_exec_flops(const GemmParams& p) {
   return f;
 }
 
-// Persistent launch in clusters of two CTAs (one 2-SM MMA pair each), as
-// many pairs as fit on the device at once, at most one per tile.
+}  // namespace
+
 // Programmatic stream serialisation for the Newton-Schulz GEMMs: a kernel so
 // launched may begin (its prologue: barriers, TMEM, tensor-map prefetch) while
 // the previous kernel of the stream finishes its last tiles; it touches global
@@ -301,11 +245,15 @@ double gemm_exec_flops(const GemmParams& p) {
 // Measured A/B on one box: one fp32 256 x 512 step 0.269 -> 0.239 ms, the MoE
 // set 98.1 -> 97.2 ms, 64 x 1024^2 1.943 -> 1.933 ms; the QK layer (projection
 // and causal max) gained nothing, so its launches keep plain stream order.
-void set_pdl(cudaLaunchAttribute& a, bool on) {
+void mc::set_pdl(cudaLaunchAttribute& a, bool on) {
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = on ? 1 : 0;
 }
 
+namespace {
+
+// Persistent launch in clusters of two CTAs (one 2-SM MMA pair each), as
+// many pairs as fit on the device at once, at most one per tile.
 template <int EPI, int WIDE>
 cudaError_t launch_pairs(const GemmParams& p, int pair_clusters, cudaStream_t s) {
   const long long pairs = std::min<long long>(pair_clusters, p.total_tiles);
@@ -1684,6 +1632,7 @@ MC_API size_t mc_struct_size(int which) {
     case 2: return sizeof(mc_normuon);
     case 3: return sizeof(mc_clip_slice);
     case 4: return sizeof(mc_kernel_stat);
+    case 16: return sizeof(mc_act8);
     default: return 0;
   }
 }

@@ -1,0 +1,469 @@
+// Weight gradients on the tensor cores: G[m, n] = sum over tokens t of
+// dY[t, m] X[t, n], for one weight or for every expert's weight, each over its
+// own rows of dY and X.
+//
+// The contraction runs over rows, so both operands are MN-major: a stage
+// holds 64 tokens as boxes of {64 columns, 64 tokens}, straight from the row-
+// major matrices by TMA, nothing is transposed in memory.  X comes as bf16,
+// exactly the values that the 8-bit form stands for (act8_unpack_kernel writes
+// them just before; they are multiples of a power of two with at most 8
+// significant bits, so this pass loses nothing).
+//
+// Execution, as in the GEMMs of umma_gemm.cuh: CTA pairs run 2-SM MMAs on
+// 256 x 256 tiles with two accumulators in TMEM, so that a tile's epilogue runs
+// under the next tile's MMAs; warp 0 issues the TMA loads, warp 1 the MMAs,
+// warps 2.. drain.  Rows behind an expert's last one must not enter its
+// gradient, not even as 0 x NaN: every expert has tensor maps of its own, made
+// on the device from the offsets, whose row extent ends with the expert, so
+// that the loads themselves fill the rest of the last 64 tokens with zeros.
+//
+// An accumulator takes at most `chunk_kb` k-blocks; a longer contraction is
+// added to the fp32 output chunk by chunk (a TMA reduction in L2, each element
+// by one thread in a fixed order).
+#pragma once
+
+#include "umma_gemm.cuh"
+
+namespace mc {
+
+struct WgradParams {
+  CUtensorMap map_a, map_b;   // one weight: dY [K][M] and X [K][N], boxes {64, 64}
+  CUtensorMap map_o;          // output [count][M][N]: boxes of 32 rows x 128 bytes
+  const CUtensorMap* maps;    // experts: [2 * count] maps of dY's and X's rows of each, else null
+  const int2* ranges;         // experts: {first row, rows} of each
+  void* out;
+  long long out_bs;           // elements from one problem's output to the next
+  long long items;            // count * tiles_m * tiles_n
+  int M, N;
+  int kb_total;               // one weight: k-blocks of the whole contraction
+  int kb_range;               // and of each of the `count` ranges that it is split into
+  int chunk_kb;
+  int tiles_m, tiles_n, band;
+  int out_f32, add, tma_out;
+  int* err;
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+// Adds this CTA's fp32 box to the tensor.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+// Makes a tensor map that an earlier kernel wrote to global memory usable by this thread's copies.
+__device__ __forceinline__ void tmap_acquire(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// ------------------------------------------------------------ experts' maps
+// One warp per expert: its row range from the offsets (clamped, so that no
+// offsets can reach outside the `rows` rows of the operands), and the two
+// tensor maps of these rows, copies of the whole operands' maps with another
+// base address and row extent.
+struct WgradMapsParams {
+  CUtensorMap map_a, map_b;
+  const int* offsets;
+  const uint8_t* a;
+  const uint8_t* b;
+  long long a_row_bytes, b_row_bytes;
+  CUtensorMap* maps;
+  int2* ranges;
+  int rows;
+};
+__global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ WgradMapsParams P) {
+  __shared__ alignas(128) CUtensorMap sm[2];
+  const int e = blockIdx.x, lane = threadIdx.x;
+  const int lo = min(max(P.offsets[e], 0), P.rows);
+  const int n = max(min(P.offsets[e + 1], P.rows) - lo, 0);
+  const uint32_t* src_a = reinterpret_cast<const uint32_t*>(&P.map_a);
+  const uint32_t* src_b = reinterpret_cast<const uint32_t*>(&P.map_b);
+  reinterpret_cast<uint32_t*>(&sm[0])[lane] = src_a[lane];
+  reinterpret_cast<uint32_t*>(&sm[1])[lane] = src_b[lane];
+  __syncwarp();
+  if (lane == 0) {
+    P.ranges[e] = make_int2(lo, n);
+    const uint64_t base[2] = {reinterpret_cast<uint64_t>(P.a) + static_cast<uint64_t>(lo) * P.a_row_bytes,
+                              reinterpret_cast<uint64_t>(P.b) + static_cast<uint64_t>(lo) * P.b_row_bytes};
+    if (n > 0) {  // an expert without rows is never loaded; its maps stay whole (a zero extent is no map)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t m = smem_u32(&sm[i]);
+        asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(m), "l"(base[i]) : "memory");
+        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(m), "r"(n) : "memory");
+      }
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+                     reinterpret_cast<uint64_t>(P.maps + 2 * e + i)),
+                 "r"(smem_u32(&sm[i]))
+                 : "memory");
+}
+
+// ------------------------------------------------------------------- tiles
+struct WgradItem {
+  int prob, tm, tn;
+  int kb_first, num_kb;
+};
+__device__ __forceinline__ WgradItem wgrad_item(const WgradParams& P, long long t) {
+  WgradItem it;
+  const long long tiles = (long long)P.tiles_m * P.tiles_n;
+  it.prob = static_cast<int>(t / tiles);
+  const int tl = static_cast<int>(t - it.prob * tiles);
+  const int per_band = P.tiles_m * P.band;
+  const int b = tl / per_band, x = tl - b * per_band;
+  const int rem = P.tiles_n - b * P.band;
+  const int w = rem < P.band ? rem : P.band;
+  it.tm = x / w;
+  it.tn = b * P.band + x % w;
+  if (P.maps) {
+    it.kb_first = 0;
+    it.num_kb = (P.ranges[it.prob].y + BK - 1) / BK;
+  } else {
+    it.kb_first = it.prob * P.kb_range;
+    it.num_kb = max(min(P.kb_range, P.kb_total - it.kb_first), 0);
+  }
+  return it;
+}
+
+constexpr size_t WGRAD_SMEM_BYTES = TileCfg<0>::SMEM_BYTES + size_t(NUM_EPI_WARPS) * EPI_BUF_BYTES;
+
+// One warp's 32 rows x 128 bytes of an accumulator to the output.  `adding`:
+// into what is there.  v: the columns of this lane's row.
+template <bool F32>
+__device__ __forceinline__ void wgrad_store(const WgradParams& P, int prob, int r0, int c0, int lane, uint8_t* buf,
+                                            const float* v, bool adding) {
+  constexpr int COLS = F32 ? 32 : 64;
+  if (P.tma_out) {
+    if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
+    __syncwarp();
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = F32 ? __float_as_uint(v[i]) : pack_bf16x2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4*>(buf + epi_swz(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (adding) {
+        tma_add_3d(&P.map_o, smem_u32(buf), c0, r0, prob);
+      } else {
+        tma_store_3d(&P.map_o, smem_u32(buf), c0, r0, prob);
+      }
+      bulk_commit_group();
+    }
+  } else if (r0 + lane < P.M) {
+    // rows that are not whole 16-byte words: element by element, each by one thread
+    const long long at = prob * P.out_bs + (long long)(r0 + lane) * P.N + c0;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) {
+      if (c0 + j < P.N) {
+        if constexpr (F32) {
+          float* o = static_cast<float*>(P.out) + at + j;
+          *o = adding ? *o + v[j] : v[j];
+        } else {
+          static_cast<__nv_bfloat16*>(P.out)[at + j] = __float2bfloat16_rn(v[j]);
+        }
+      }
+    }
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __grid_constant__ WgradParams P) {
+  using T = TileCfg<0>;
+  constexpr int STAGES = T::STAGES;
+  constexpr int NACC = T::NACC;
+  constexpr uint32_t STAGE_BYTES = T::STAGE_BYTES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + size_t(NUM_EPI_WARPS) * EPI_BUF_BYTES);
+  uint64_t* full_bar = bars;                           // [STAGES]  used in the leader only
+  uint64_t* empty_bar = bars + STAGES;                 // [STAGES]  every CTA
+  uint64_t* tfull_bar = bars + 2 * STAGES;             // [NACC]    every CTA
+  uint64_t* tempty_bar = bars + 2 * STAGES + NACC;     // [NACC]    used in the leader only
+  uint64_t* drain_bar = bars + 2 * STAGES + 2 * NACC;  // [1]       leader
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * STAGES + 2 * NACC + 1) * 8 + 8 <= GEMM_BARRIER_BYTES, "barrier block");
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0 = leader (issues the MMAs)
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < NACC; ++b) {
+      mbar_init(smem_u32(&tfull_bar[b]), 1);
+      mbar_init(smem_u32(&tempty_bar[b]), 2 * NUM_EPI_WARPS);
+    }
+    mbar_init(smem_u32(drain_bar), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    if (!P.maps) {
+      prefetch_tmap(&P.map_a);
+      prefetch_tmap(&P.map_b);
+    }
+    if (P.tma_out) prefetch_tmap(&P.map_o);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+  const long long first_item = blockIdx.x >> 1;
+  const long long item_step = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t filled = 0, fill_parity = 0;
+      bool ok = true;
+      int mapped = -1;
+      for (long long t = first_item; ok && t < P.items; t += item_step) {
+        const WgradItem it = wgrad_item(P, t);
+        const CUtensorMap* ma = P.maps ? P.maps + 2 * it.prob : &P.map_a;
+        const CUtensorMap* mb = P.maps ? P.maps + 2 * it.prob + 1 : &P.map_b;
+        if (P.maps && mapped != it.prob) {
+          tmap_acquire(ma);
+          tmap_acquire(mb);
+          mapped = it.prob;
+        }
+        const int m0 = it.tm * BM + HALF * static_cast<int>(rank);
+        const int n0 = it.tn * T::N + HALF * static_cast<int>(rank);
+        // stages do not straddle chunks: the MMA side counts them the same way
+        for (int c0 = 0; ok && c0 < it.num_kb; c0 += P.chunk_kb) {
+          const int c1 = min(c0 + P.chunk_kb, it.num_kb);
+          for (int kb0 = c0; kb0 < c1; kb0 += T::KPS) {
+            const int nk = min(c1 - kb0, T::KPS);
+            if (!wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1, abort_flag, P.err)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb_local = smem_u32(&full_bar[stage]);
+            if (leader) {
+              mbar_arrive_expect_tx(fb_local, uint32_t(nk) * T::PAIR_KB_BYTES);
+              filled |= 1u << stage;
+              fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+            }
+            const uint32_t fb = mapa_shared(fb_local, 0);
+            for (int j = 0; j < nk; ++j) {
+              const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES + j * T::KB_BYTES);
+              const uint32_t sb = sa + A_STAGE_BYTES;
+              const int k0 = (it.kb_first + kb0 + j) * BK;
+              tma_load_2d_pair(sa, ma, fb, m0, k0);
+              tma_load_2d_pair(sa + MN_BOX_BYTES, ma, fb, m0 + 64, k0);
+              tma_load_2d_pair(sb, mb, fb, n0, k0);
+              tma_load_2d_pair(sb + MN_BOX_BYTES, mb, fb, n0 + 64, k0);
+            }
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      }
+      // every copy of the pair lands before anyone leaves
+      if (leader)
+        for (int s = 0; s < STAGES; ++s)
+          if (filled & (1u << s)) {
+            volatile int no_abort = 0;
+            wait_bounded(smem_u32(&full_bar[s]), (fill_parity >> s) & 1u, &no_abort, nullptr, kDrainLimitCycles);
+          }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer (leader)
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      const uint32_t s0 = smem_u32(smem);
+      const uint32_t idesc = idesc_bf16_f32(BM, MMA_N, 1, 1);
+      const uint64_t ad0 = smem_desc_sw128(s0, MN_BOX_BYTES, 1024);
+      const uint64_t bd0 = smem_desc_sw128(s0 + A_STAGE_BYTES, MN_BOX_BYTES, 1024);
+      for (long long t = first_item; ok && t < P.items; t += item_step) {
+        const WgradItem it = wgrad_item(P, t);
+        for (int c0 = 0; ok && c0 < it.num_kb; c0 += P.chunk_kb) {
+          const int c1 = min(c0 + P.chunk_kb, it.num_kb);
+          if (!wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1, abort_flag, P.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * T::N;
+          for (int kb0 = c0; kb0 < c1; kb0 += T::KPS) {
+            const int nk = min(c1 - kb0, T::KPS);
+            if (!wait_bounded(smem_u32(&full_bar[stage]), phase, abort_flag, P.err)) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int j = 0; j < T::KPS; ++j) {
+              if (j >= nk) break;
+              const uint64_t soff = static_cast<uint64_t>((stage * STAGE_BYTES + j * T::KB_BYTES) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const uint64_t koff = soff + ((kk * 16u * 128u) >> 4);
+                umma_bf16_pair(d_tmem, ad0 + koff, bd0 + koff, idesc, ((kb0 - c0 + j) | kk) != 0);
+              }
+            }
+            umma_commit_pair_mc(smem_u32(&empty_bar[stage]), 0x3);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          umma_commit_pair_mc(smem_u32(&tfull_bar[acc]), 0x3);
+          if (++acc == NACC) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
+        }
+      }
+      // every MMA of the pair completes before TMEM is released
+      umma_commit_pair(smem_u32(drain_bar));
+      volatile int no_abort = 0;
+      wait_bounded(smem_u32(drain_bar), 0, &no_abort, nullptr, kDrainLimitCycles);
+    }
+  } else {
+    // ------------------------------------------------------- epilogue
+    constexpr int WCOLS = T::N / EPI_COL_GROUPS;  // columns per epilogue warp
+    constexpr int COLS = F32 ? 32 : 64;           // columns per store
+    const int q = warp & 3;                       // TMEM lane quarter this warp may read
+    const int half = (warp - 2) >> 2;             // which column group of the tile
+    uint8_t* buf = smem + STAGES * STAGE_BYTES + (warp - 2) * EPI_BUF_BYTES;
+    uint32_t tempty_leader[NACC];
+#pragma unroll
+    for (int b = 0; b < NACC; ++b) tempty_leader[b] = mapa_shared(smem_u32(&tempty_bar[b]), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (long long t = first_item; ok && t < P.items; t += item_step) {
+      const WgradItem it = wgrad_item(P, t);
+      const int r0 = it.tm * BM + HALF * static_cast<int>(rank) + q * 32;
+      const int cbase = it.tn * T::N + half * WCOLS;
+      float v[COLS];
+      if (it.num_kb == 0) {  // no rows: the gradient is zero
+        if (!P.add && r0 < P.M) {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) v[j] = 0.f;
+          for (int cb = 0; cb < WCOLS && cbase + cb < P.N; cb += COLS)
+            wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
+        }
+        continue;
+      }
+      for (int c0 = 0; c0 < it.num_kb; c0 += P.chunk_kb) {
+        // every lane waits; the warp goes on only if all of them saw the phase complete
+        const bool got = wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, P.err);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * T::N + half * WCOLS;
+        const bool adding = P.add || c0 > 0;
+        if (c0 > 0) {  // what this warp wrote of the earlier chunks is in memory before it is added to
+          if (lane == 0) bulk_wait_all();
+          __syncwarp();
+        }
+        if (r0 < P.M) {
+#pragma unroll 1
+          for (int cb = 0; cb < WCOLS; cb += COLS) {
+            if (cbase + cb >= P.N) break;
+            if constexpr (F32) {
+              tmem_ld16(t_row + cb, *reinterpret_cast<float(*)[16]>(v));
+              tmem_ld16(t_row + cb + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+            } else {
+              tmem_ld64(t_row + cb, v);
+            }
+            wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, adding);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
+        if (++acc == NACC) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // stores complete before the CTA's shared memory is released
+    __syncwarp();
+  }
+
+  // Nobody leaves (or frees TMEM) while the peer may still signal this CTA's
+  // barriers or read its shared memory.
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------- split contraction
+// G = (G +) sum of the ranges' partial products, ranges in order.
+template <typename T>
+__global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict__ part, T* __restrict__ out, int M, int N,
+                                                         int ldp, int ranges, int add) {
+  const long long bs = (long long)M * ldp;
+  for (long long r = blockIdx.y; r < M; r += gridDim.y) {
+    for (int c = (blockIdx.x * 256 + threadIdx.x) * 4; c < N; c += gridDim.x * 1024) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < ranges; ++p) {
+        const float4 v = *reinterpret_cast<const float4*>(part + p * bs + r * ldp + c);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      const float t[4] = {s.x, s.y, s.z, s.w};
+      T* o = out + r * N + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (c + i < N) {
+          if constexpr (sizeof(T) == 4) {
+            o[i] = add ? o[i] + t[i] : t[i];
+          } else {
+            o[i] = __float2bfloat16_rn(t[i]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// dY with rows that TMA cannot step over (not whole 16-byte words), to rows of `ld` elements.
+__global__ void __launch_bounds__(256) wgrad_copy_kernel(const __nv_bfloat16* __restrict__ src, __nv_bfloat16* __restrict__ dst,
+                                                         long long rows, int cols, int ld) {
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256) dst[r * ld + c] = src[r * cols + c];
+}
+
+}  // namespace mc

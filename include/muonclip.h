@@ -542,10 +542,10 @@ int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, const mc
  * mc_weight_grad -- the gradient of an nn.Linear weight (rows = out-features)
  * from its output's gradient and its input kept in 8 bits:
  *   g[m][n] = sum over rows r of dy[r][m] * x[r][n]        (accumulate: added to g)
- * on tensor cores, with x's values exact in bf16 and fp32 accumulation; an fp32
- * sum is carried over at most 4096 rows inside the tensor cores, then in fp32
- * registers of the memory system or in ranges joined in order.  Results do not
- * depend on anything but the operands and their sizes.
+ * on tensor cores, with x's values exact in bf16 and fp32 accumulation.  For an
+ * fp32 g, sums are carried over 1024 rows inside the tensor cores and added
+ * beyond that with rounding to nearest, in a fixed order.  Results depend on
+ * nothing but the operands and their sizes.
  * dy     device bf16, x->rows x out_features
  * g      device, out_features x x->cols, g_dtype; accumulate needs MC_F32
  * x->rows == 0 gives g = 0 (accumulate: unchanged).
@@ -559,10 +559,11 @@ int mc_weight_grad(const void* dy, const mc_act8* x, int64_t out_features, void*
  * mc_expert_weight_grad -- mc_weight_grad of every expert's weight in one call:
  *   g[e][m][n] = sum over rows r in [offsets[e], offsets[e + 1]) of dy[r][m] * x[row(r)][n]
  * dy       device bf16, rows x out_features, rows sorted by expert (mc_expert_sort)
- * x        row(r) = r (source NULL: x has `rows` rows, sorted like dy), or
- *          row(r) = source[r] / top_k (x has rows / top_k rows, in token order; an
- *          entry that names none of them counts as a row of zeros)
- * offsets  device int32 [experts + 1]; taken into [0, rows] where they are not
+ * x        position NULL: row(r) = r, x has `rows` rows, sorted like dy; else x has
+ *          rows / top_k rows in token order, and row(position[t][k]) = t
+ * offsets, position  device int32 [experts + 1] and [rows / top_k][top_k], of one
+ *          mc_expert_sort; offsets are taken into [0, rows] and entries of position
+ *          outside it count as dropped
  * g        device, experts x out_features x x->cols, g_dtype; accumulate needs MC_F32.
  *          An expert without rows gets zeros (accumulate: is left as it is).
  * Rows of dy outside every expert are not read into any result, whatever they hold.
@@ -570,8 +571,8 @@ int mc_weight_grad(const void* dy, const mc_act8* x, int64_t out_features, void*
  * workspace  >= mc_expert_weight_grad_workspace_size(...), or NULL.
  */
 size_t mc_expert_weight_grad_workspace_size(int64_t rows, int experts, int64_t out_features, int64_t in_features);
-int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int32_t* offsets, const int32_t* source,
-                          int top_k, int experts, int64_t out_features, void* g, int g_dtype, int accumulate,
+int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int32_t* offsets,
+                          const int32_t* position, int top_k, int experts, int64_t out_features, void* g, int g_dtype, int accumulate,
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*

@@ -50,31 +50,45 @@ class ExpertPlan(NamedTuple):
     position: "torch.Tensor"
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, without a Stream object
+
+
 class _On:
     """Runs a block with the device, and the stream if one is given, current."""
-    __slots__ = ("cm",)
+    __slots__ = ("cm", "index")
 
     def __init__(self, device, stream):
+        self.cm = None
+        self.index = device.index
         if stream is not None:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
             self.cm = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
+        elif self.index != torch.cuda.current_device():
             self.cm = torch.cuda.device(device)
-        else:
-            self.cm = None
 
     def __enter__(self):
         if self.cm is not None:
             self.cm.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         if self.cm is not None:
             self.cm.__exit__(*exc)
 
 
+def _one_dev(first, *others):
+    """The device of ``first``; raises unless every other (non-None) tensor is on it."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            _one_device([first, *others])
+    return dev
+
+
 def _rows_cols(shape):
+    if len(shape) == 2:
+        return shape[0], shape[1]
     rows = 1
     for n in shape[:-1]:
         rows *= int(n)
@@ -82,45 +96,57 @@ def _rows_cols(shape):
 
 
 def _need_matrix(t, name):
-    _need_cuda_contig(t, name)
+    if not (t.is_cuda and t.is_contiguous()):
+        _need_cuda_contig(t, name)
     if t.dim() < 1 or t.shape[-1] < 1:
         raise ValueError(f"{name} must have at least one column, got shape {tuple(t.shape)}")
 
 
 def _fmt_code(fmt):
-    if fmt not in _FMT:
+    code = _FMT.get(fmt)
+    if code is None:
         raise ValueError(f"fmt must be 'e4m3' or 'int8', got {fmt!r}")
-    return _FMT[fmt]
+    return code
 
 
 def _act8_struct(a, name):
-    q, s = a.q, a.scale
-    code = _fmt_code(a.fmt)
-    for t, nm in ((q, "q"), (s, "scale")):
-        if not t.is_cuda:
-            raise ValueError(f"{name}.{nm} must be a CUDA tensor")
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{name}.{nm} must be uint8")
-        if t.dim() != 2 or not t.is_contiguous():
-            raise ValueError(f"{name}.{nm} must be a contiguous 2D tensor")
-    if len(a.shape) < 1 or int(a.shape[-1]) < 1:
-        raise ValueError(f"{name}.shape must have at least one column, got {tuple(a.shape)}")
-    rows, cols = _rows_cols(a.shape)
-    if q.shape[0] != rows or s.shape[0] != rows:
-        raise ValueError(f"{name}: q and scale must have {rows} rows, got {q.shape[0]} and {s.shape[0]}")
-    if q.shape[1] < cols or q.shape[1] % 16 or s.shape[1] * ACT_BLOCK < cols or s.shape[1] % 16:
+    q, s, shape, fmt = a
+    code = _fmt_code(fmt)
+    u8 = torch.uint8
+    if not (q.is_cuda and s.is_cuda):
+        raise ValueError(f"{name}.q and {name}.scale must be CUDA tensors")
+    if not (q.dtype is u8 and s.dtype is u8):
+        raise TypeError(f"{name}.q and {name}.scale must be uint8")
+    qs, ss = q.shape, s.shape
+    if not (len(qs) == 2 and len(ss) == 2 and q.is_contiguous() and s.is_contiguous()):
+        raise ValueError(f"{name}.q and {name}.scale must be contiguous 2D tensors")
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError(f"{name}.shape must have at least one column, got {tuple(shape)}")
+    rows, cols = _rows_cols(shape)
+    if qs[0] != rows or ss[0] != rows:
+        raise ValueError(f"{name}: q and scale must have {rows} rows, got {qs[0]} and {ss[0]}")
+    if qs[1] < cols or qs[1] % 16 or ss[1] * ACT_BLOCK < cols or ss[1] % 16:
         raise ValueError(f"{name}: rows of q and scale must be whole 16 bytes and hold {cols} columns, "
-                         f"got {q.shape[1]} and {s.shape[1]} bytes")
-    return McAct8(q.data_ptr(), s.data_ptr(), rows, cols, q.shape[1], s.shape[1], code, 0)
+                         f"got {qs[1]} and {ss[1]} bytes")
+    return McAct8(q.data_ptr(), s.data_ptr(), rows, cols, qs[1], ss[1], code, 0)
+
+
+def _act8_new(shape, rows, cols, fmt, dev):
+    """An unset Act8 of checked arguments, and its structure."""
+    q_ld = (cols + 15) & ~15
+    s_ld = ((cols + ACT_BLOCK - 1) // ACT_BLOCK + 15) & ~15
+    q = torch.empty((rows, q_ld), dtype=torch.uint8, device=dev)
+    s = torch.empty((rows, s_ld), dtype=torch.uint8, device=dev)
+    return Act8(q, s, shape, fmt), McAct8(q.data_ptr(), s.data_ptr(), rows, cols, q_ld, s_ld, _FMT[fmt], 0)
 
 
 def act8_empty(shape, fmt: str = "int8", device=None) -> Act8:
     """An Act8 of this shape with unset contents."""
     _fmt_code(fmt)
-    rows, cols = _rows_cols(shape)
-    nb = -(-cols // ACT_BLOCK)
-    return Act8(torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device or "cuda"),
-                torch.empty((rows, -(-nb // 16) * 16), dtype=torch.uint8, device=device or "cuda"), tuple(shape), fmt)
+    shape = tuple(int(n) for n in shape)
+    if len(shape) < 1 or shape[-1] < 1 or min(shape) < 0:
+        raise ValueError(f"shape must have at least one column, got {shape}")
+    return _act8_new(shape, *_rows_cols(shape), fmt, device or "cuda")[0]
 
 
 def act8_pack(x, fmt: str = "int8", *, out: Act8 = None, stream=None) -> Act8:
@@ -129,13 +155,18 @@ def act8_pack(x, fmt: str = "int8", *, out: Act8 = None, stream=None) -> Act8:
     lib = load_library()
     _need_matrix(x, "x")
     code = _dtype_code(x)
-    dev = _one_device([x] if out is None else [x, out.q, out.scale])
+    shape = tuple(x.shape)
+    if out is None:
+        _fmt_code(fmt)
+        dev = x.device
+    else:
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out must have x's shape {shape}, got {tuple(out.shape)}")
+        a = _act8_struct(out, "out")
+        dev = _one_dev(x, out.q, out.scale)
     with _On(dev, stream) as s:
         if out is None:
-            out = act8_empty(x.shape, fmt, dev)
-        elif tuple(out.shape) != tuple(x.shape):
-            raise ValueError(f"out must have x's shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        a = _act8_struct(out, "out")
+            out, a = _act8_new(shape, *_rows_cols(shape), fmt, dev)
         _check(lib.mc_act8_pack(x.data_ptr(), code, ctypes.byref(a), s))
     return out
 
@@ -144,7 +175,7 @@ def act8_unpack(a: Act8, *, dtype=None, out=None, stream=None):
     """The values of an Act8 as bf16 (exact for whatever act8_pack or rms_norm wrote) or fp32."""
     lib = load_library()
     st = _act8_struct(a, "a")
-    dev = _one_device([a.q, a.scale, out])
+    dev = _one_dev(a.q, a.scale, out)
     with _On(dev, stream) as s:
         if out is None:
             out = torch.empty(a.shape, dtype=dtype or torch.bfloat16, device=dev)
@@ -165,7 +196,7 @@ def rms_norm(x, weight, *, residual=None, eps: float = 1e-6, fmt: str = None, h_
     _need_matrix(x, "x")
     _need_matrix(weight, "weight")
     rows, cols = _rows_cols(x.shape)
-    if tuple(weight.shape) != (cols,):
+    if weight.shape != (cols,):
         raise ValueError(f"weight must have shape ({cols},), got {tuple(weight.shape)}")
     for t, nm in ((residual, "residual"), (h_out, "h_out")):
         if t is not None:
@@ -175,7 +206,9 @@ def rms_norm(x, weight, *, residual=None, eps: float = 1e-6, fmt: str = None, h_
     if h_out is not None and residual is None:
         raise ValueError("h_out goes with residual: without one, h is x")
     code, wcode = _dtype_code(x), _dtype_code(weight)
-    dev = _one_device([x, weight, residual, h_out])
+    if fmt is not None:
+        _fmt_code(fmt)
+    dev = _one_dev(x, weight, residual, h_out)
     with _On(dev, stream) as s:
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
         if residual is not None and h_out is None:
@@ -184,8 +217,8 @@ def rms_norm(x, weight, *, residual=None, eps: float = 1e-6, fmt: str = None, h_
             y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
             yp, y8 = y.data_ptr(), None
         else:
-            y = act8_empty(x.shape, fmt, dev)
-            yp, y8 = None, ctypes.byref(_act8_struct(y, "y"))
+            y, st = _act8_new(tuple(x.shape), rows, cols, fmt, dev)
+            yp, y8 = None, ctypes.byref(st)
         _check(lib.mc_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), code, wcode, rows, cols, float(eps),
                                _ptr(h_out), yp, y8, rstd.data_ptr(), s))
     return RmsNorm(x if residual is None else h_out, y, rstd)
@@ -201,7 +234,7 @@ def rms_norm_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, workspace=No
     _need_matrix(weight, "weight")
     _need_cuda_contig(rstd, "rstd")
     rows, cols = _rows_cols(dy.shape)
-    if tuple(weight.shape) != (cols,):
+    if weight.shape != (cols,):
         raise ValueError(f"weight must have shape ({cols},), got {tuple(weight.shape)}")
     if rstd.dtype != torch.float32 or rstd.numel() != rows:
         raise ValueError(f"rstd must be float32 with {rows} entries")
@@ -214,14 +247,14 @@ def rms_norm_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, workspace=No
         if _rows_cols(h.shape) != (rows, cols):
             raise ValueError(f"h must have dy's shape {tuple(dy.shape)}, got {tuple(h.shape)}")
         st = _act8_struct(h, "h")
-        hp, h8, held = None, ctypes.byref(st), [h.q, h.scale]
+        hp, h8, held = None, ctypes.byref(st), (h.q, h.scale)
     else:
         _need_matrix(h, "h")
         if h.shape != dy.shape or h.dtype != dy.dtype:
             raise ValueError("h must have dy's shape and type")
-        hp, h8, held = h.data_ptr(), None, [h]
+        hp, h8, held = h.data_ptr(), None, (h,)
     code, wcode = _dtype_code(dy), _dtype_code(weight)
-    dev = _one_device([dy, weight, rstd, dh, dx_out, workspace] + held)
+    dev = _one_dev(dy, weight, rstd, dh, dx_out, workspace, *held)
     with _On(dev, stream) as s:
         dx = torch.empty_like(dy) if dx_out is None else dx_out
         dw = torch.empty(cols, dtype=torch.float32, device=dev)
@@ -268,7 +301,7 @@ def weight_grad(dy, x: Act8, *, dtype=None, out=None, accumulate: bool = False, 
     rows, M = _rows_cols(dy.shape)
     if rows != st.rows:
         raise ValueError(f"dy and x must have the same rows, got {rows} and {st.rows}")
-    dev = _one_device([dy, x.q, x.scale, out, workspace])
+    dev = _one_dev(dy, x.q, x.scale, out, workspace)
     with _On(dev, stream) as s:
         g = _grad_out(out, (M, st.cols), dtype, accumulate, dev)
         ws, nbytes = _scratch(workspace, lib.mc_weight_grad_workspace_size(rows, M, st.cols), dev)
@@ -278,15 +311,17 @@ def weight_grad(dy, x: Act8, *, dtype=None, out=None, accumulate: bool = False, 
 
 
 def _check_plan(plan):
-    for t, nm in ((plan.offsets, "offsets"), (plan.source, "source"), (plan.position, "position")):
-        _need_cuda_contig(t, f"plan.{nm}")
-        if t.dtype != torch.int32:
+    off, src, pos = plan
+    i32 = torch.int32
+    for t, nm in ((off, "offsets"), (src, "source"), (pos, "position")):
+        if not (t.is_cuda and t.is_contiguous()):
+            _need_cuda_contig(t, f"plan.{nm}")
+        if t.dtype is not i32:
             raise TypeError(f"plan.{nm} must be int32")
-    if plan.position.dim() != 2 or plan.position.shape[1] < 1 or plan.offsets.dim() != 1 or plan.offsets.numel() < 2 or \
-            tuple(plan.source.shape) != (plan.position.numel(),):
+    shape = pos.shape
+    if len(shape) != 2 or shape[1] < 1 or off.dim() != 1 or off.shape[0] < 2 or src.shape != (shape[0] * shape[1],):
         raise ValueError("plan must hold offsets [E + 1], source [T * K] and position [T, K]")
-    T, K = plan.position.shape
-    return int(T), int(K), int(plan.offsets.numel()) - 1
+    return shape[0], shape[1], off.shape[0] - 1
 
 
 def expert_sort(idx, num_experts: int, *, workspace=None, stream=None) -> ExpertPlan:
@@ -300,7 +335,7 @@ def expert_sort(idx, num_experts: int, *, workspace=None, stream=None) -> Expert
         raise ValueError(f"idx must be 2D [T, K], got shape {tuple(idx.shape)}")
     T, K = int(idx.shape[0]), int(idx.shape[1])
     E = int(num_experts)
-    dev = _one_device([idx, workspace])
+    dev = _one_dev(idx, workspace)
     with _On(dev, stream) as s:
         # one allocation for the three results (each on a 16-byte boundary)
         n, o = -(-T * K // 4) * 4, -(-(max(E, 0) + 1) // 4) * 4
@@ -336,7 +371,7 @@ def expert_gather(x, plan: ExpertPlan, *, out=None, stream=None):
     T, K, _ = _check_plan(plan)
     _check_rows(x, "x", T)
     code, D = _dtype_code(x), int(x.shape[1])
-    dev = _one_device([x, plan.position, out])
+    dev = _one_dev(x, plan.position, out)
     with _On(dev, stream) as s:
         if out is None:
             out = torch.empty((T * K, D), dtype=x.dtype, device=dev)
@@ -355,7 +390,7 @@ def expert_combine(y, plan: ExpertPlan, weights=None, *, out=None, stream=None):
     if weights is not None:
         _check_weights(weights, T, K)
     code, D = _dtype_code(y), int(y.shape[1])
-    dev = _one_device([y, plan.position, weights, out])
+    dev = _one_dev(y, plan.position, weights, out)
     with _On(dev, stream) as s:
         if out is None:
             out = torch.empty((T, D), dtype=y.dtype, device=dev)
@@ -375,7 +410,7 @@ def expert_combine_backward(dout, y, plan: ExpertPlan, weights, *, out=None, str
     code, D = _dtype_code(dout), int(dout.shape[1])
     _check_rows(y, "y", T * K, D, dout.dtype)
     _check_weights(weights, T, K)
-    dev = _one_device([dout, y, plan.position, weights, out])
+    dev = _one_dev(dout, y, plan.position, weights, out)
     with _On(dev, stream) as s:
         if out is None:
             out = torch.empty((T * K, D), dtype=y.dtype, device=dev)
@@ -402,11 +437,11 @@ def expert_weight_grad(dy, x: Act8, plan: ExpertPlan, *, gather: bool, dtype=Non
     st = _act8_struct(x, "x")
     if st.rows != (T if gather else rows):
         raise ValueError(f"x must have {T if gather else rows} rows, got {st.rows}")
-    dev = _one_device([dy, x.q, x.scale, plan.offsets, plan.source, out, workspace])
+    dev = _one_dev(dy, x.q, x.scale, plan.offsets, plan.position, out, workspace)
     with _On(dev, stream) as s:
         g = _grad_out(out, (E, M, st.cols), dtype, accumulate, dev)
         ws, nbytes = _scratch(workspace, lib.mc_expert_weight_grad_workspace_size(rows, E, M, st.cols), dev)
         _check(lib.mc_expert_weight_grad(dy.data_ptr(), rows, ctypes.byref(st), plan.offsets.data_ptr(),
-                                         plan.source.data_ptr() if gather else None, K, E, M, g.data_ptr(), _dtype_code(g),
+                                         plan.position.data_ptr() if gather else None, K, E, M, g.data_ptr(), _dtype_code(g),
                                          int(bool(accumulate)), ws.data_ptr(), nbytes, s))
     return g

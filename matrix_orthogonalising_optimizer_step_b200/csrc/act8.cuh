@@ -300,14 +300,11 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restr
   }
 }
 
-// Rows of an 8-bit activation to bf16 or fp32.  With `source` (rows sorted by
-// expert): output row r is row source[r] / top_k of the activation's `a_rows`;
-// an entry that names none of them gives a row of zeros.
+// The rows of an 8-bit activation to bf16 or fp32.
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t* __restrict__ q,
                                                                   const uint8_t* __restrict__ s, T* __restrict__ out,
-                                                                  const int* __restrict__ source, int top_k,
-                                                                  long long rows, long long a_rows, int D, long long q_ld,
+                                                                  long long rows, int D, long long q_ld,
                                                                   long long s_ld, long long out_ld, int chunks) {
   constexpr int UNROLL = 4;
   const int lane = threadIdx.x & 31;
@@ -322,15 +319,7 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       at[u] = w;
-      f[u] = Raw8{make_uint2(0u, 0u), make_uint2(0u, 0u)};
-      if (w.row < rows) {
-        long long from = w.row;
-        if (source) {
-          const int p = source[w.row];
-          from = p < 0 ? a_rows : p / top_k;
-        }
-        if (from < a_rows) load_frag8<VEC>(f[u], q + from * q_ld, s + from * s_ld, w.chunk * WARP_COLS, lane, D);
-      }
+      if (w.row < rows) load_frag8<VEC>(f[u], q + w.row * q_ld, s + w.row * s_ld, w.chunk * WARP_COLS, lane, D);
       walk_next(w, step_rows, step_chunks, chunks);
     }
 #pragma unroll
@@ -339,6 +328,53 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
       float v[8];
       frag8_floats<FMT, VEC>(f[u], at[u].chunk * WARP_COLS, lane, D, v);
       store_frag<VEC>(out + at[u].row * out_ld, at[u].chunk * WARP_COLS, lane, D, v);
+    }
+  }
+}
+
+// Rows in token order to their pairs' sorted rows in bf16: output row
+// position[t * top_k + k] is row t, for every pair that is not dropped.  A token's
+// codes are read and converted once for all its rows.  out_ld is a multiple of
+// 8 and the bytes up to it may be written, whatever D.
+template <int FMT>
+__global__ void __launch_bounds__(ACT_THREADS) act8_scatter_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
+                                                                   __nv_bfloat16* __restrict__ out,
+                                                                   const int* __restrict__ position, int top_k, long long tokens,
+                                                                   int D, long long q_ld, long long s_ld, long long out_ld,
+                                                                   int segments) {
+  constexpr int RUNS = 4;  // 256-column runs of an item
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
+  const long long first = (long long)blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);
+  const long long step_rows = warps / segments;
+  const int step_seg = static_cast<int>(warps % segments);
+  const long long rows = tokens * top_k;
+  RowWalk w{first / segments, static_cast<int>(first % segments)};
+  for (; w.row < tokens; walk_next(w, step_rows, step_seg, segments)) {
+    const int c0 = w.chunk * RUNS * WARP_COLS;
+    Raw8 f[RUNS];
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u)
+      load_frag8<true>(f[u], q + w.row * q_ld, s + w.row * s_ld, c0 + u * WARP_COLS, lane, D);
+    uint4 v[RUNS];
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+      float x[8];
+      frag8_floats<FMT, true>(f[u], c0 + u * WARP_COLS, lane, D, x);
+      v[u] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    for (int k0 = 0; k0 < top_k; k0 += 32) {
+      const int mine = k0 + lane < top_k ? position[w.row * top_k + k0 + lane] : -1;
+      const int kn = min(32, top_k - k0);
+      for (int k = 0; k < kn; ++k) {
+        const int r = __shfl_sync(0xffffffffu, mine, k);
+        if (r < 0 || r >= rows) continue;
+#pragma unroll
+        for (int u = 0; u < RUNS; ++u) {
+          const int c = c0 + u * WARP_COLS + 8 * lane;
+          if (c < D) *reinterpret_cast<uint4*>(out + r * out_ld + c) = v[u];
+        }
+      }
     }
   }
 }

@@ -77,16 +77,16 @@ void pack_launch(const void* x, const mc_act8* a, int chunks, unsigned blocks, c
       static_cast<int>(a->cols), a->q_ld, a->s_ld, chunks);
 }
 template <typename T, int FMT, bool VEC>
-void unpack_launch(const mc_act8* a, void* out, const int* source, int top_k, int64_t rows, int64_t out_ld, int chunks,
+void unpack_launch(const mc_act8* a, void* out, int64_t rows, int64_t out_ld, int chunks,
                    unsigned blocks, cudaStream_t s) {
   act8_unpack_kernel<T, FMT, VEC><<<blocks, ACT_THREADS, 0, s>>>(
-      static_cast<const uint8_t*>(a->q), static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), source, top_k, rows,
-      a->rows, static_cast<int>(a->cols), a->q_ld, a->s_ld, out_ld, chunks);
+      static_cast<const uint8_t*>(a->q), static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), rows,
+      static_cast<int>(a->cols), a->q_ld, a->s_ld, out_ld, chunks);
 }
 
-// Rows of `a` (or its rows source[r] / top_k) to `out`, rows of out_ld elements.
-int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, const int* source, int top_k, int64_t rows,
-           int64_t out_ld, bool vec, int kind, cudaStream_t s) {
+// The rows of `a` to `out`, rows of out_ld elements.
+int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, int64_t out_ld, bool vec, int kind, cudaStream_t s) {
+  const int64_t rows = a->rows;
   if (rows == 0) return MC_OK;
   const int chunks = static_cast<int>((a->cols + WARP_COLS - 1) / WARP_COLS);
   const unsigned blocks = item_blocks(rows * chunks, 4, ACT_THREADS / 32, st.sms, 8);
@@ -95,8 +95,8 @@ int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, const 
   auto go = [&](auto t, auto v) {
     using T = decltype(t);
     constexpr bool V = decltype(v)::value;
-    if (e4) unpack_launch<T, ACT_E4M3, V>(a, out, source, top_k, rows, out_ld, chunks, blocks, s);
-    else unpack_launch<T, ACT_INT8, V>(a, out, source, top_k, rows, out_ld, chunks, blocks, s);
+    if (e4) unpack_launch<T, ACT_E4M3, V>(a, out, rows, out_ld, chunks, blocks, s);
+    else unpack_launch<T, ACT_INT8, V>(a, out, rows, out_ld, chunks, blocks, s);
   };
   if (dtype == MC_F32) {
     if (vec) go(float{}, std::true_type{});
@@ -179,7 +179,7 @@ int check_norm(const void* w, int dtype, int w_dtype, int64_t rows, int64_t cols
 
 // ------------------------------------------------------------ weight gradient
 // Longest contraction one accumulator takes for an fp32 output.
-constexpr int kWgradChunkKb = 64;
+constexpr int kWgradChunkKb = 16;
 
 struct WgradPlan {
   int64_t ldx, ldy, ldp;     // rows of the bf16 X, of dY, of a partial product
@@ -241,10 +241,9 @@ int act_device_state(DeviceState** out) {
   const int rc = device_state(out);
   if (rc != MC_OK) return rc;
   if (!(*out)->act_init) {
-    MC_CUDA(cudaFuncSetAttribute(weight_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(WGRAD_SMEM_BYTES)));
-    MC_CUDA(cudaFuncSetAttribute(weight_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(WGRAD_SMEM_BYTES)));
+    const int gemm_smem = static_cast<int>(WGRAD_SMEM_BYTES);
+    MC_CUDA(cudaFuncSetAttribute(weight_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem));
+    MC_CUDA(cudaFuncSetAttribute(weight_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem));
     const int sort_smem = (SORT_WARPS + 2) * (MAX_EXPERTS + 1) * 4;
     MC_CUDA(cudaFuncSetAttribute(expert_place_kernel<int>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem));
     MC_CUDA(cudaFuncSetAttribute(expert_place_kernel<long long>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem));
@@ -273,7 +272,7 @@ int check_wgrad(const void* dy, const mc_act8* x, int64_t rows, int64_t M, const
 }
 
 // G (one weight: offsets NULL) or every expert's G.  Caller holds g_mu.
-int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offsets, const int* source, int top_k,
+int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offsets, const int* position, int top_k,
                 int experts, int64_t M, void* g, int g_dtype, int accumulate, void* workspace, size_t workspace_bytes,
                 cudaStream_t s) {
   DeviceState* st = nullptr;
@@ -321,7 +320,21 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
     P.ranges = mp.ranges;
   }
   // rows of the workspace are padded to whole 16 bytes, so this always takes the wide path
-  if ((rc = unpack(*st, x, ws + p.off_x, MC_BF16, source, top_k, rows, p.ldx, true, K_WGRAD_PREP, s)) != MC_OK) return rc;
+  if (position) {
+    const int segments = static_cast<int>((N + 4 * WARP_COLS - 1) / (4 * WARP_COLS));
+    const unsigned blocks = item_blocks(x->rows * segments, 1, ACT_THREADS / 32, st->sms, 8);
+    ProfScope prof(K_WGRAD_PREP, s, 0, 0, double(x->rows) * N * (1 + 1.0 / ACT_BLOCK) + 2.0 * double(rows) * N);
+    auto go = [&](auto kernel) {
+      kernel<<<blocks, ACT_THREADS, 0, s>>>(static_cast<const uint8_t*>(x->q), static_cast<const uint8_t*>(x->scale),
+                                            reinterpret_cast<__nv_bfloat16*>(ws + p.off_x), position, top_k, x->rows,
+                                            static_cast<int>(N), x->q_ld, x->s_ld, p.ldx, segments);
+    };
+    if (x->fmt == MC_ACT_E4M3) go(act8_scatter_kernel<ACT_E4M3>);
+    else go(act8_scatter_kernel<ACT_INT8>);
+    MC_CUDA(cudaGetLastError());
+  } else if ((rc = unpack(*st, x, ws + p.off_x, MC_BF16, p.ldx, true, K_WGRAD_PREP, s)) != MC_OK) {
+    return rc;
+  }
 
   const bool split = p.ranges > 1;
   P.M = static_cast<int>(M);
@@ -463,7 +476,7 @@ MC_API int mc_act8_unpack(const mc_act8* a, void* out, int out_dtype, void* stre
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   if ((rc = act_device_state(&st)) != MC_OK) return rc;
-  return unpack(*st, a, out, out_dtype, nullptr, 1, a->rows, a->cols, a->cols % 8 == 0, K_ACT_UNPACK,
+  return unpack(*st, a, out, out_dtype, a->cols, a->cols % 8 == 0, K_ACT_UNPACK,
                 static_cast<cudaStream_t>(stream));
 }
 
@@ -659,7 +672,7 @@ MC_API size_t mc_expert_weight_grad_workspace_size(int64_t rows, int experts, in
   return wgrad_plan(rows, out_features, in_features, experts).total;
 }
 
-MC_API int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int32_t* offsets, const int32_t* source,
+MC_API int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int32_t* offsets, const int32_t* position,
                                  int top_k, int experts, int64_t out_features, void* g, int g_dtype, int accumulate,
                                  void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_act8(x);
@@ -667,20 +680,20 @@ MC_API int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x,
   if ((rc = check_wgrad(dy, x, rows, out_features, g, g_dtype, accumulate)) != MC_OK) return rc;
   if (experts < 1 || experts > MAX_EXPERTS) return fail(MC_ERR_INVAL, "experts must be in [1, 1024]");
   if (!offsets) return fail(MC_ERR_INVAL, "NULL offsets");
-  if (source) {
+  if (position) {
     if (top_k < 1 || top_k > MAX_EXPERTS) return fail(MC_ERR_INVAL, "top_k must be in [1, 1024]");
     if (x->rows > kMaxRows / top_k || x->rows * top_k != rows)
-      return fail(MC_ERR_INVAL, "with source, rows must be top_k times the rows of x");
+      return fail(MC_ERR_INVAL, "with position, rows must be top_k times the rows of x");
   } else if (x->rows != rows) {
-    return fail(MC_ERR_INVAL, "without source, x must have the rows of dy");
+    return fail(MC_ERR_INVAL, "without position, x must have the rows of dy");
   }
-  if (!aligned16(offsets) || !aligned16(source)) return fail(MC_ERR_ALIGN, "pointers must be 16-byte aligned");
+  if (!aligned16(offsets) || !aligned16(position)) return fail(MC_ERR_ALIGN, "pointers must be 16-byte aligned");
   const int64_t gb = int64_t(experts) * out_features * x->cols * dtype_bytes(g_dtype);
   if (meets(g, gb, dy, 2 * rows * out_features) || meets(g, gb, x->q, q_bytes(x)) || meets(g, gb, x->scale, s_bytes(x)) ||
-      meets(g, gb, offsets, 4 * (experts + 1)) || meets(g, gb, source, 4 * rows))
+      meets(g, gb, offsets, 4 * (experts + 1)) || meets(g, gb, position, 4 * rows))
     return fail(MC_ERR_INVAL, "g must not overlap the inputs");
   std::lock_guard<std::mutex> lock(g_mu);
-  return weight_grad(dy, rows, x, offsets, source, source ? top_k : 1, experts, out_features, g, g_dtype, accumulate, workspace,
+  return weight_grad(dy, rows, x, offsets, position, position ? top_k : 1, experts, out_features, g, g_dtype, accumulate, workspace,
                      workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 

@@ -134,10 +134,10 @@ def test_expert_refusals_and_workspace(lib):
                 dict(dy=Y + 16), dict(dw=W), dict(dw=X)):
         assert back(**bad) == mc.MC_ERR_INVAL, bad
 
-    def grad(dy=X, rows=16, a=None, off=Y, src=Z, K=2, E=8, M=64, g=W, dt=mc.MC_F32, acc=0):
-        return lib.mc_expert_weight_grad(dy, rows, P(a or act8()), off, src, K, E, M, g, dt, acc, None, 0, None)
-    for bad in (dict(off=None), dict(rows=15), dict(K=0), dict(K=3), dict(E=0), dict(E=1025), dict(src=None),
-                dict(src=None, rows=9), dict(g=X), dict(g=Y), dict(dt=mc.MC_BF16, acc=1)):
+    def grad(dy=X, rows=16, a=None, off=Y, pos=Z, K=2, E=8, M=64, g=W, dt=mc.MC_F32, acc=0):
+        return lib.mc_expert_weight_grad(dy, rows, P(a or act8()), off, pos, K, E, M, g, dt, acc, None, 0, None)
+    for bad in (dict(off=None), dict(rows=15), dict(K=0), dict(K=3), dict(E=0), dict(E=1025), dict(pos=None),
+                dict(pos=None, rows=9), dict(g=X), dict(g=Y), dict(dt=mc.MC_BF16, acc=1)):
         assert grad(**bad) == mc.MC_ERR_INVAL, bad
     assert grad(off=Y + 4) == mc.MC_ERR_ALIGN
 

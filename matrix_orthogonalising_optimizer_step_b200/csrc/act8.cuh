@@ -127,6 +127,33 @@ __device__ __forceinline__ void store_frag(float* row, int c0, int lane, int D, 
   }
 }
 
+// Values rounded to the fragment's type, and the fragment as it is to memory.
+__device__ __forceinline__ void frag_round(RawFrag<__nv_bfloat16>& f, const float (&v)[8]) {
+  f.q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void frag_round(RawFrag<float>& f, const float (&v)[8]) {
+  f.a = make_float4(v[0], v[1], v[2], v[3]);
+  f.b = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_raw(T* row, int c0, int lane, int D, const RawFrag<T>& f) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    const int c = c0 + 8 * lane;
+    if (c < D) *reinterpret_cast<uint4*>(row + c) = f.q;
+  } else {
+    float v[8];
+    frag_floats(f, v);
+    store_frag<VEC>(row, c0, lane, D, v);
+  }
+}
+
+// max(|a|, |b|), NaN if either is
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 // ------------------------------------------------------------------- codes
 // k of a block whose largest |x| has these bits; any finite value.
 template <int FMT>
@@ -170,11 +197,10 @@ __device__ __forceinline__ float2 act_decode2(uint32_t two) {
 template <int FMT, bool VEC>
 __device__ __forceinline__ void store_frag8(uint8_t* qrow, uint8_t* srow, int c0, int lane, int D, const float (&v)[8]) {
   if constexpr (VEC) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    float big = max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])), max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])));
+    big = max_abs(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = max_abs(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const uint32_t m = __float_as_uint(big);
     const bool fine = m < 0x7F800000u;
     const int k = act_exponent<FMT>(m);
     const float r = exp2_int(-k);

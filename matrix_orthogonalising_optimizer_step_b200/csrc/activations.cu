@@ -144,6 +144,37 @@ NormShape norm_bwd_shape(int64_t cols) {
 }
 constexpr int kNormBwdBlocks = 640;  // most blocks of the gradient's walk
 
+// The gradient through the shared-memory ring.  wpr = 0: the row does not fit.
+constexpr int kNormRingBytes = 100 * 1024;      // of a block of 8 warps: two of them share an SM
+constexpr int kNormRingBytesWide = 200 * 1024;  // of a block of up to 16
+NormShape norm_ring_shape(int64_t cols, int64_t row_bytes, int64_t q_row, int64_t s_row, bool dh, NormRing* R) {
+  const int frags = static_cast<int>((cols + WARP_COLS - 1) / WARP_COLS);
+  NormShape n;
+  n.nv = frags <= 8 ? 1 : (frags <= 16 ? 2 : 4);
+  n.wpr = (frags + n.nv - 1) / n.nv;
+  n.groups = std::max(1, 8 / n.wpr);
+  n.threads = 32 * n.wpr * n.groups;
+  auto at = [](int64_t b) { return (b + 127) / 128 * 128; };
+  const int64_t rows_b = at(n.groups * row_bytes);
+  const int64_t h_b = q_row ? at(n.groups * q_row) + at(n.groups * s_row) : rows_b;
+  const int64_t stage = rows_b * (dh ? 2 : 1) + h_b;
+  const int64_t room = n.wpr <= 8 ? kNormRingBytes : kNormRingBytesWide;
+  const int64_t stages = std::min<int64_t>(NORM_RING_STAGES, room / stage);
+  if (n.wpr > 16 || stages < 2) {
+    n.wpr = 0;
+    return n;
+  }
+  R->stages = static_cast<int>(stages);
+  R->stage_bytes = static_cast<int>(stage);
+  R->off_dh = static_cast<int>(rows_b);
+  R->off_h = static_cast<int>(rows_b * (dh ? 2 : 1));
+  R->off_s = static_cast<int>(R->off_h + at(n.groups * q_row));
+  R->row_bytes = static_cast<int>(row_bytes);
+  R->q_row = static_cast<int>(q_row);
+  R->s_row = static_cast<int>(s_row);
+  return n;
+}
+
 template <typename F>
 void with_nv(int nv, F&& f) {
   if (nv == 1) f(std::integral_constant<int, 1>{});
@@ -554,9 +585,12 @@ MC_API int mc_rms_norm(const void* x, const void* residual, const void* w, int d
 
 MC_API size_t mc_rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (rows < 0 || rows > kMaxRows || cols < 1 || cols > NORM_MAX_COLS) return 0;
-  const NormShape sh = norm_bwd_shape(cols);
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((rows + sh.groups - 1) / sh.groups, kNormBwdBlocks));
-  return align_up(size_t(blocks) * sh.groups * cols * sizeof(float), 256);
+  // a part is the sum of one group of warps; either form of the kernel has at
+  // most 8 / ceil(fragments / 4) groups a block
+  const int64_t frags = (cols + WARP_COLS - 1) / WARP_COLS;
+  const int64_t groups = std::max<int64_t>(1, 8 / ((frags + 3) / 4));
+  const int64_t parts = std::min<int64_t>(std::max<int64_t>(rows, 1) + groups - 1, kNormBwdBlocks * groups);
+  return align_up(size_t(parts) * cols * sizeof(float), 256);
 }
 
 MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, const mc_act8* h8, const void* w,
@@ -592,6 +626,9 @@ MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, c
     return MC_OK;
   }
   if ((rc = take_workspace(st, mc_rms_norm_backward_workspace_size(rows, cols), &workspace, workspace_bytes)) != MC_OK) return rc;
+  const int64_t q_row = h8 ? (cols + 15) / 16 * 16 : 0, s_row = h8 ? ((cols + ACT_BLOCK - 1) / ACT_BLOCK + 15) / 16 * 16 : 0;
+  NormRing ring = {};
+  const NormShape rs = cols % 8 == 0 ? norm_ring_shape(cols, cols * dtype_bytes(dtype), q_row, s_row, dh != nullptr, &ring) : NormShape{};
   const NormShape sh = norm_bwd_shape(cols);
   int parts = 0;
   cudaError_t err = cudaSuccess;
@@ -613,9 +650,27 @@ MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, c
       a.q_ld = h8 ? h8->q_ld : 0;
       a.s_ld = h8 ? h8->s_ld : 0;
       a.D = static_cast<int>(cols);
-      a.wpr = sh.wpr;
+      a.wpr = rs.wpr ? rs.wpr : sh.wpr;
       a.w_f32 = w_dtype == MC_F32 ? 1 : 0;
       with_fmt(h8 ? h8->fmt : -1, [&](auto f) {
+        if (rs.wpr) {
+          auto launch = [&](auto kernel, int per_sm) {
+            const int smem = ring.stages * ring.stage_bytes;
+            if (smem > 40 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (err != cudaSuccess) return;
+            const unsigned blocks = static_cast<unsigned>(
+                std::min<int64_t>((rows + rs.groups - 1) / rs.groups, std::min<int64_t>(kNormBwdBlocks, int64_t(per_sm) * st->sms)));
+            parts = static_cast<int>(blocks) * rs.groups;
+            kernel<<<blocks, rs.threads + 32, smem, s>>>(a, ring, st->err_ptr);
+          };
+          constexpr int F = decltype(f)::value;
+          if (rs.threads > 256) {
+            launch(rms_norm_bwd_ring_kernel<T, F, 4, 512>, 1);
+          } else {
+            with_nv(rs.nv, [&](auto nv) { launch(rms_norm_bwd_ring_kernel<T, F, decltype(nv)::value, 256>, 2); });
+          }
+          return;
+        }
         with_bool(cols % 8 == 0, [&](auto v) {
           auto launch = [&](auto kernel) {
             int per_sm = 0;

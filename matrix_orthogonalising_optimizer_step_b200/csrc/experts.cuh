@@ -344,13 +344,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* _
 // One block per token: its 8 warps share the row, every pair's dot product is
 // kept by thread over the whole row and joined at the end (lanes by a tree,
 // then warps in order).  dy may be y itself: a thread reads what it overwrites.
+// Four pairs' loads are in flight at a time; more would cost the registers
+// that let three blocks share an SM (all eight at once: one block, 260 us for
+// 4096 tokens of 8 pairs of 7168 bf16 columns; so: see the launch's figure).
 constexpr int BACK_PAIRS = 8;  // pairs whose sums a pass over the row keeps
+constexpr int BACK_AHEAD = 4;  // pairs loaded together
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(MOVE_THREADS) expert_combine_bwd_kernel(const T* __restrict__ dout, const T* y,
-                                                                          const int* __restrict__ position,
-                                                                          const float* __restrict__ weights, T* dy,
-                                                                          float* __restrict__ dweights, long long tokens, int K,
-                                                                          int D) {
+__global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(const T* __restrict__ dout, const T* y,
+                                                                             const int* __restrict__ position,
+                                                                             const float* __restrict__ weights, T* dy,
+                                                                             float* __restrict__ dweights, long long tokens, int K,
+                                                                             int D) {
   constexpr int N = move_elems<T>();
   constexpr int WARPS = MOVE_THREADS / 32;
   __shared__ float part[WARPS][BACK_PAIRS];
@@ -358,35 +362,42 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_bwd_kernel(const 
   const long long rows = tokens * K;
   for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
     for (int k0 = 0; k0 < K; k0 += BACK_PAIRS) {
-      int pos[BACK_PAIRS];
-      float wk[BACK_PAIRS], dot[BACK_PAIRS];
-#pragma unroll
-      for (int a = 0; a < BACK_PAIRS; ++a) {
-        const bool in = k0 + a < K;
-        pos[a] = in ? position[t * K + k0 + a] : -1;
-        if (pos[a] >= rows) pos[a] = -1;
-        wk[a] = in ? weights[t * K + k0 + a] : 0.f;
-        dot[a] = 0.f;
+      // lane a < BACK_PAIRS holds pair k0 + a's row and weight
+      int mine = -1;
+      float wmine = 0.f;
+      if (lane < BACK_PAIRS && k0 + lane < K) {
+        mine = position[t * K + k0 + lane];
+        if (mine >= rows) mine = -1;
+        wmine = weights[t * K + k0 + lane];
       }
+      float dot[BACK_PAIRS];
+#pragma unroll
+      for (int a = 0; a < BACK_PAIRS; ++a) dot[a] = 0.f;
       for (int c0 = warp * run_cols<T>(); c0 < D; c0 += WARPS * run_cols<T>()) {
-        const uint4 g = move_load<T, VEC>(dout + t * D, c0, lane, D);
-        uint4 q[BACK_PAIRS];
+        float g[N];
+        move_floats<T>(move_load<T, VEC>(dout + t * D, c0, lane, D), g);
 #pragma unroll
-        for (int a = 0; a < BACK_PAIRS; ++a)
-          if (pos[a] >= 0) q[a] = move_load<T, VEC>(y + (long long)pos[a] * D, c0, lane, D);
-        float gv[N];
-        move_floats<T>(g, gv);
+        for (int a0 = 0; a0 < BACK_PAIRS; a0 += BACK_AHEAD) {
+          uint4 q[BACK_AHEAD];
+          int pos[BACK_AHEAD];
 #pragma unroll
-        for (int a = 0; a < BACK_PAIRS; ++a) {
-          if (pos[a] < 0) continue;
-          float v[N];
-          move_floats<T>(q[a], v);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[a] = fmaf(gv[i], v[i], dot[a]);
-            v[i] = wk[a] * gv[i];
+          for (int a = 0; a < BACK_AHEAD; ++a) {
+            pos[a] = __shfl_sync(0xffffffffu, mine, a0 + a);
+            if (pos[a] >= 0) q[a] = move_load<T, VEC>(y + (long long)pos[a] * D, c0, lane, D);
           }
-          move_store<T, VEC>(dy + (long long)pos[a] * D, c0, lane, D, move_words<T>(v));
+#pragma unroll
+          for (int a = 0; a < BACK_AHEAD; ++a) {
+            const float wk = __shfl_sync(0xffffffffu, wmine, a0 + a);
+            if (pos[a] < 0) continue;
+            float v[N];
+            move_floats<T>(q[a], v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dot[a0 + a] = fmaf(g[i], v[i], dot[a0 + a]);
+              v[i] = wk * g[i];
+            }
+            move_store<T, VEC>(dy + (long long)pos[a] * D, c0, lane, D, move_words<T>(v));
+          }
         }
       }
 #pragma unroll

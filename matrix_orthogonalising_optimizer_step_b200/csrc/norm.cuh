@@ -21,7 +21,8 @@ constexpr int NORM_MAX_THREADS = 1024;
 constexpr int NORM_MAX_COLS = 32768;  // 1024 threads x 4 fragments x 8 columns
 
 // Sum over the `wpr` warps that share a row; every thread of the block calls it.
-__device__ __forceinline__ float row_sum(float v, int wpr, float* buf) {
+template <typename F>
+__device__ __forceinline__ F row_sum(F v, int wpr, F* buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (wpr == 1) return v;
@@ -29,9 +30,35 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float* buf) {
   if ((threadIdx.x & 31) == 0) buf[warp] = v;
   __syncthreads();
   const int w0 = warp / wpr * wpr;
-  float t = 0.f;
+  F t = 0;
   for (int i = 0; i < wpr; ++i) t += buf[w0 + i];
   return t;
+}
+
+// 1 / sqrt(m) to about 2^-43: the fp32 estimate and one Newton step; outside
+// its range (and for m = 0, infinities and NaN) the library's square root.
+__device__ __forceinline__ double rsqrt64(double m) {
+  if (m > 1e-37 && m < 1e38) {
+    const double r = rsqrtf(static_cast<float>(m));
+    return r * (1.5 - 0.5 * m * r * r);
+  }
+  return 1.0 / sqrt(m);
+}
+
+// x * r * w for an 8-bit output, as fp32 rounded to odd: r is given as
+// r_hi + r_lo, the product is kept to about 2^-46, and a result that is not
+// exact is moved to the neighbour with an odd last bit.  A rounding to 8 bits
+// of it is the rounding of the exact product (a value just beside the middle
+// of two codes never looks like the middle), so the codes are those of the
+// formula wherever the row's sum is.  Infinities and NaN pass through.
+__device__ __forceinline__ float scaled_to_odd(float x, float w, float r_hi, float r_lo) {
+  const float t_hi = r_hi * w;
+  const float t_lo = fmaf(r_lo, w, fmaf(r_hi, w, -t_hi));
+  const float y = x * t_hi;
+  const float e = fmaf(x, t_lo, fmaf(x, t_hi, -y));
+  const int bits = __float_as_int(y);
+  const int toward = ((bits ^ __float_as_int(e)) >> 31) | 1;  // +1: the exact product is larger in magnitude
+  return __int_as_float(bits + ((fabsf(e) > 0.f && (bits & 1) == 0) ? toward : 0));
 }
 
 // The norm's weight of one fragment (bf16 or fp32), 0 past D.
@@ -63,59 +90,71 @@ struct NormFwdArgs {
   float eps;
 };
 
+// The sum of squares is kept in 64 bits (an fp32 square is exact there): its
+// error would move every value of the row the same way.  B200 adds at half the
+// fp32 rate there, and the memory leaves room for it.
 template <typename T, int FMT, bool VEC, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormFwdArgs<T> a) {
-  __shared__ float buf[32];
+  __shared__ double buf[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = (blockDim.x >> 5) / a.wpr;
   const long long row = (long long)blockIdx.x * groups + warp / a.wpr;
   const int wr = warp % a.wpr;
   const bool live = row < a.rows;
   const long long base = row * a.D;
-  float v[NV][8];
-  float sum = 0.f;
+  RawFrag<T> f[NV];
+  double sum = 0.0;
   if (live) {
-    RawFrag<T> fx[NV], fr[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_frag<VEC>(fx[j], a.x + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D);
+    for (int j = 0; j < NV; ++j) load_frag<VEC>(f[j], a.x + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D);
     if (a.r) {
+      RawFrag<T> fr[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) load_frag<VEC>(fr[j], a.r + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float v[8], t[8];
+        frag_floats(f[j], v);
+        frag_floats(fr[j], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += t[i];
+        frag_round(f[j], v);  // the norm sees h as the next layers will: in the stored type
+        store_raw<VEC>(a.h + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D, f[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      frag_floats(fx[j], v[j]);
-      if (a.r) {
-        float t[8];
-        frag_floats(fr[j], t);
+      float v[8];
+      frag_floats(f[j], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[j][i] += t[i];
-          // the norm sees h as the next layers will: rounded to the stored type
-          if constexpr (sizeof(T) == 2) v[j][i] = __bfloat162float(__float2bfloat16_rn(v[j][i]));
-        }
-        store_frag<VEC>(a.h + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D, v[j]);
+      for (int i = 0; i < 8; ++i) {
+        const double d = v[i];
+        sum = fma(d, d, sum);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i], v[j][i], sum);
     }
   }
   sum = row_sum(sum, a.wpr, buf);
   if (!live) return;
-  const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.D) + a.eps);
+  const double r64 = rsqrt64(sum / static_cast<double>(a.D) + static_cast<double>(a.eps));
+  const float rstd = static_cast<float>(r64);
+  const float r_lo = static_cast<float>(r64 - static_cast<double>(rstd));
   if (wr == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c0 = (j * a.wpr + wr) * WARP_COLS;
     if (c0 >= a.D) break;
-    float w[8];
+    float v[8], w[8];
+    frag_floats(f[j], v);
     load_weight<VEC>(a.w, a.w_f32, c0, lane, a.D, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] = frag_col<VEC>(c0, lane, i) < a.D ? v[j][i] * rstd * w[i] : 0.f;
+    // columns past D hold x = w = 0
     if constexpr (FMT == ACT_NONE) {
-      store_frag<VEC>(a.y + base, c0, lane, a.D, v[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * w[i];
+      store_frag<VEC>(a.y + base, c0, lane, a.D, v);
     } else {
-      store_frag8<FMT, VEC>(a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D, v[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i], w[i], rstd, r_lo);
+      store_frag8<FMT, VEC>(a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D, v);
     }
   }
 }
@@ -258,6 +297,197 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
       if (c < a.D) out[c] = dw[j][i];
     }
   }
+}
+
+// The same for rows of whole 16-byte words that fit in shared memory: a
+// producer warp copies rows (bulk asynchronous copies) into a ring of stages, as
+// many as the shared memory of half an SM holds, and the other warps read them
+// twice from there, for the row's sum and for its output, so that what is in
+// flight does not depend on registers.  dw and the weight stay in registers.
+// A stage holds one row for each of the block's groups of `wpr` warps.
+struct NormRing {
+  int stages, stage_bytes;
+  int off_dh, off_h, off_s;             // of a stage's dh rows, h rows (or codes) and scale bytes (dy at 0)
+  int row_bytes, q_row, s_row;          // bytes of a row of dy, of codes, of scale bytes
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Barrier of one group of warps; returns whether any of its threads brought `p`,
+// the same answer to all of them (so that they leave a loop together).
+__device__ __forceinline__ bool group_any(int id, int threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %3, 0;\n\t"
+      "barrier.cta.red.or.pred b, %1, %2, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(p ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+constexpr int NORM_RING_STAGES = 8;
+template <typename T, int FMT, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm_bwd_ring_kernel(const NormBwdArgs<T> a, const NormRing R,
+                                                                                             int* err) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full_bar[NORM_RING_STAGES], empty_bar[NORM_RING_STAGES];
+  __shared__ float buf[2][32];
+  __shared__ int abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int workers = (blockDim.x >> 5) - 1;
+  const int groups = workers / a.wpr;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R.stages; ++i) {
+      mbar_init(smem_u32(&full_bar[i]), 1);
+      mbar_init(smem_u32(&empty_bar[i]), workers);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const long long step = (long long)gridDim.x * groups;
+  if (warp == workers) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, filled = 0, parity = 0;
+      for (long long row = (long long)blockIdx.x * groups; row < a.rows; row += step) {
+        if (!wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1, &abort_flag, err)) break;
+        const int n = static_cast<int>(min(static_cast<long long>(groups), a.rows - row));
+        const uint32_t dst = smem_u32(ring) + stage * R.stage_bytes, bar = smem_u32(&full_bar[stage]);
+        const uint32_t rows_bytes = static_cast<uint32_t>(n) * R.row_bytes;
+        mbar_arrive_expect_tx(bar, rows_bytes * (a.dh ? 2u : 1u) +
+                                       (FMT == ACT_NONE ? rows_bytes : static_cast<uint32_t>(n) * (R.q_row + R.s_row)));
+        bulk_load(dst, a.dy + row * a.D, rows_bytes, bar);
+        if (a.dh) bulk_load(dst + R.off_dh, a.dh + row * a.D, rows_bytes, bar);
+        if constexpr (FMT == ACT_NONE) {
+          bulk_load(dst + R.off_h, a.h + row * a.D, rows_bytes, bar);
+        } else {
+          for (int g = 0; g < n; ++g) {
+            bulk_load(dst + R.off_h + g * R.q_row, a.q + (row + g) * a.q_ld, R.q_row, bar);
+            bulk_load(dst + R.off_s + g * R.s_row, a.s + (row + g) * a.s_ld, R.s_row, bar);
+          }
+        }
+        filled |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == R.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // every copy lands before the block leaves
+      for (int i = 0; i < R.stages; ++i)
+        if (filled & (1u << i)) {
+          volatile int no_abort = 0;
+          wait_bounded(smem_u32(&full_bar[i]), (parity >> i) & 1u, &no_abort, nullptr, kDrainLimitCycles);
+        }
+    }
+    return;
+  }
+  // --------------------------------------------------------------- workers
+  const int group = warp / a.wpr, wr = warp % a.wpr;
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  float dw[NV][8], w[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    load_weight<true>(a.w, a.w_f32, (j * a.wpr + wr) * WARP_COLS, lane, a.D, w[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  }
+  int stage = 0, flip = 0;
+  uint32_t phase = 0;
+  for (long long first = (long long)blockIdx.x * groups; first < a.rows; first += step) {
+    const long long row = first + group;
+    bool live = row < a.rows;
+    const uint8_t* st = ring + stage * R.stage_bytes;
+    const T* s_dy = reinterpret_cast<const T*>(st + group * R.row_bytes);
+    const T* s_dh = reinterpret_cast<const T*>(st + R.off_dh + group * R.row_bytes);
+    const T* s_h = reinterpret_cast<const T*>(st + R.off_h + group * R.row_bytes);
+    const uint8_t* s_q = st + R.off_h + group * R.q_row;
+    const uint8_t* s_s = st + R.off_s + group * R.s_row;
+    const float rstd = live ? a.rstd[row] : 0.f;
+    const bool got = __all_sync(0xffffffffu, wait_bounded(smem_u32(&full_bar[stage]), phase, &abort_flag, err));
+    live = live && got;
+    auto values = [&](int c0, float (&dy)[8], float (&xhat)[8]) {
+      RawFrag<T> f;
+      load_frag<true>(f, s_dy, c0, lane, a.D);
+      frag_floats(f, dy);
+      if constexpr (FMT == ACT_NONE) {
+        load_frag<true>(f, s_h, c0, lane, a.D);
+        frag_floats(f, xhat);
+      } else {
+        Raw8 q;
+        load_frag8<true>(q, s_q, s_s, c0, lane, a.D);
+        frag8_floats<FMT, true>(q, c0, lane, a.D, xhat);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xhat[i] *= rstd;
+    };
+    float dot = 0.f;
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c0 = (j * a.wpr + wr) * WARP_COLS;
+        if (c0 >= a.D) break;
+        float dy[8], xhat[8];
+        values(c0, dy, xhat);  // zeros past D
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = dy[i] * xhat[i];
+          dw[j][i] += p;
+          dot = fmaf(p, w[j][i], dot);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (a.wpr > 1) {
+      // two buffers in turn, as above; the groups go their own pace
+      if (lane == 0) buf[flip][warp] = dot;
+      if (group_any(1 + group, 32 * a.wpr, !got)) break;
+      dot = 0.f;
+      for (int i = 0; i < a.wpr; ++i) dot += buf[flip][group * a.wpr + i];
+      flip ^= 1;
+    } else if (!got) {
+      break;
+    }
+    const float c = dot * inv_d;
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c0 = (j * a.wpr + wr) * WARP_COLS;
+        if (c0 >= a.D) break;
+        float dy[8], xhat[8], o[8];
+        values(c0, dy, xhat);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = rstd * fmaf(-xhat[i], c, dy[i] * w[j][i]);
+        if (a.dh) {
+          RawFrag<T> f;
+          float t[8];
+          load_frag<true>(f, s_dh, c0, lane, a.D);
+          frag_floats(f, t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += t[i];
+        }
+        store_frag<true>(a.dx + row * a.D, c0, lane, a.D, o);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
+    if (++stage == R.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  float* out = a.partial + ((long long)blockIdx.x * groups + group) * a.D;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) store_frag<true>(out, (j * a.wpr + wr) * WARP_COLS, lane, a.D, dw[j]);
 }
 
 // dw[c] = sum of the partial rows, each column's in a fixed order: warp w of a

@@ -16,8 +16,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (MC_F32, MC_BF16, McAct8, MC_ACT_E4M3, MC_ACT_INT8, _check, _check_out, _dtype_code, _need_cuda_contig,
-               _one_device, _ptr, load_library)
+from . import (McAct8, MC_ACT_E4M3, MC_ACT_INT8, _check, _dtype_code, _need_cuda_contig, _one_device, _ptr,
+               load_library)
 
 ACT_BLOCK = 32
 _FMT = {"e4m3": MC_ACT_E4M3, "int8": MC_ACT_INT8}
@@ -50,31 +50,24 @@ class ExpertPlan(NamedTuple):
     position: "torch.Tensor"
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, without a Stream object
+# The current stream's handle and the current device, without a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-class _On:
-    """Runs a block with the device, and the stream if one is given, current."""
-    __slots__ = ("cm", "index")
-
-    def __init__(self, device, stream):
-        self.cm = None
-        self.index = device.index
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.cm = torch.cuda.stream(stream)
-        elif self.index != torch.cuda.current_device():
-            self.cm = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.cm is not None:
-            self.cm.__enter__()
-        return _raw_stream(self.index)
-
-    def __exit__(self, *exc):
-        if self.cm is not None:
-            self.cm.__exit__(*exc)
+def _enter(device, stream):
+    """Makes the device (and the stream, if one is given) current; returns what
+    has to be left again, or None where nothing had to be done."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        cm = torch.cuda.stream(stream)
+    elif device.index == _current_device():
+        return None
+    else:
+        cm = torch.cuda.device(device)
+    cm.__enter__()
+    return cm
 
 
 def _one_dev(first, *others):
@@ -98,8 +91,15 @@ def _rows_cols(shape):
 def _need_matrix(t, name):
     if not (t.is_cuda and t.is_contiguous()):
         _need_cuda_contig(t, name)
-    if t.dim() < 1 or t.shape[-1] < 1:
+    shape = t.shape
+    if not shape or shape[-1] < 1:
         raise ValueError(f"{name} must have at least one column, got shape {tuple(t.shape)}")
+
+
+def _need_like(t, name, other, other_name):
+    _need_cuda_contig(t, name)
+    if t.shape != other.shape or t.dtype != other.dtype:
+        raise ValueError(f"{name} must have {other_name}'s shape and type")
 
 
 def _fmt_code(fmt):
@@ -135,8 +135,8 @@ def _act8_new(shape, rows, cols, fmt, dev):
     """An unset Act8 of checked arguments, and its structure."""
     q_ld = (cols + 15) & ~15
     s_ld = ((cols + ACT_BLOCK - 1) // ACT_BLOCK + 15) & ~15
-    q = torch.empty((rows, q_ld), dtype=torch.uint8, device=dev)
-    s = torch.empty((rows, s_ld), dtype=torch.uint8, device=dev)
+    q = torch.empty(rows, q_ld, dtype=torch.uint8, device=dev)
+    s = torch.empty(rows, s_ld, dtype=torch.uint8, device=dev)
     return Act8(q, s, shape, fmt), McAct8(q.data_ptr(), s.data_ptr(), rows, cols, q_ld, s_ld, _FMT[fmt], 0)
 
 
@@ -164,10 +164,15 @@ def act8_pack(x, fmt: str = "int8", *, out: Act8 = None, stream=None) -> Act8:
             raise ValueError(f"out must have x's shape {shape}, got {tuple(out.shape)}")
         a = _act8_struct(out, "out")
         dev = _one_dev(x, out.q, out.scale)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         if out is None:
             out, a = _act8_new(shape, *_rows_cols(shape), fmt, dev)
         _check(lib.mc_act8_pack(x.data_ptr(), code, ctypes.byref(a), s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return out
 
 
@@ -176,14 +181,19 @@ def act8_unpack(a: Act8, *, dtype=None, out=None, stream=None):
     lib = load_library()
     st = _act8_struct(a, "a")
     dev = _one_dev(a.q, a.scale, out)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         if out is None:
-            out = torch.empty(a.shape, dtype=dtype or torch.bfloat16, device=dev)
+            out = torch.empty(*a.shape, dtype=dtype or torch.bfloat16, device=dev)
         else:
             _need_matrix(out, "out")
             if tuple(out.shape) != tuple(a.shape) or (dtype is not None and out.dtype != dtype):
                 raise ValueError(f"out must have shape {tuple(a.shape)}" + (f" and type {dtype}" if dtype else ""))
         _check(lib.mc_act8_unpack(ctypes.byref(st), out.data_ptr(), _dtype_code(out), s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return out
 
 
@@ -194,33 +204,38 @@ def rms_norm(x, weight, *, residual=None, eps: float = 1e-6, fmt: str = None, h_
     ``h_out`` may be x or residual itself."""
     lib = load_library()
     _need_matrix(x, "x")
-    _need_matrix(weight, "weight")
-    rows, cols = _rows_cols(x.shape)
+    _need_cuda_contig(weight, "weight")
+    shape = x.shape
+    rows, cols = _rows_cols(shape)
     if weight.shape != (cols,):
         raise ValueError(f"weight must have shape ({cols},), got {tuple(weight.shape)}")
-    for t, nm in ((residual, "residual"), (h_out, "h_out")):
-        if t is not None:
-            _need_matrix(t, nm)
-            if t.shape != x.shape or t.dtype != x.dtype:
-                raise ValueError(f"{nm} must have x's shape and type")
+    if residual is not None:
+        _need_like(residual, "residual", x, "x")
+    if h_out is not None:
+        _need_like(h_out, "h_out", x, "x")
     if h_out is not None and residual is None:
         raise ValueError("h_out goes with residual: without one, h is x")
     code, wcode = _dtype_code(x), _dtype_code(weight)
     if fmt is not None:
         _fmt_code(fmt)
     dev = _one_dev(x, weight, residual, h_out)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
         if residual is not None and h_out is None:
             h_out = torch.empty_like(x)
         if fmt is None:
-            y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+            y = torch.empty_like(x, dtype=torch.bfloat16)
             yp, y8 = y.data_ptr(), None
         else:
-            y, st = _act8_new(tuple(x.shape), rows, cols, fmt, dev)
+            y, st = _act8_new(tuple(shape), rows, cols, fmt, dev)
             yp, y8 = None, ctypes.byref(st)
         _check(lib.mc_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), code, wcode, rows, cols, float(eps),
                                _ptr(h_out), yp, y8, rstd.data_ptr(), s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return RmsNorm(x if residual is None else h_out, y, rstd)
 
 
@@ -231,45 +246,47 @@ def rms_norm_backward(dy, h, weight, rstd, *, dh=None, dx_out=None, workspace=No
     ``dx_out`` may be dy or dh itself."""
     lib = load_library()
     _need_matrix(dy, "dy")
-    _need_matrix(weight, "weight")
+    _need_cuda_contig(weight, "weight")
     _need_cuda_contig(rstd, "rstd")
     rows, cols = _rows_cols(dy.shape)
     if weight.shape != (cols,):
         raise ValueError(f"weight must have shape ({cols},), got {tuple(weight.shape)}")
     if rstd.dtype != torch.float32 or rstd.numel() != rows:
         raise ValueError(f"rstd must be float32 with {rows} entries")
-    for t, nm in ((dh, "dh"), (dx_out, "dx_out")):
-        if t is not None:
-            _need_matrix(t, nm)
-            if t.shape != dy.shape or t.dtype != dy.dtype:
-                raise ValueError(f"{nm} must have dy's shape and type")
+    if dh is not None:
+        _need_like(dh, "dh", dy, "dy")
+    if dx_out is not None:
+        _need_like(dx_out, "dx_out", dy, "dy")
     if isinstance(h, Act8):
         if _rows_cols(h.shape) != (rows, cols):
             raise ValueError(f"h must have dy's shape {tuple(dy.shape)}, got {tuple(h.shape)}")
         st = _act8_struct(h, "h")
         hp, h8, held = None, ctypes.byref(st), (h.q, h.scale)
     else:
-        _need_matrix(h, "h")
-        if h.shape != dy.shape or h.dtype != dy.dtype:
-            raise ValueError("h must have dy's shape and type")
+        _need_like(h, "h", dy, "dy")
         hp, h8, held = h.data_ptr(), None, (h,)
     code, wcode = _dtype_code(dy), _dtype_code(weight)
     dev = _one_dev(dy, weight, rstd, dh, dx_out, workspace, *held)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         dx = torch.empty_like(dy) if dx_out is None else dx_out
         dw = torch.empty(cols, dtype=torch.float32, device=dev)
         ws, nbytes = _scratch(workspace, lib.mc_rms_norm_backward_workspace_size(rows, cols), dev)
         _check(lib.mc_rms_norm_backward(dy.data_ptr(), _ptr(dh), hp, h8, weight.data_ptr(), rstd.data_ptr(), code, wcode,
                                         rows, cols, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), nbytes, s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return dx, dw
 
 
 def _scratch(workspace, need, dev):
     """The caller's workspace, or scratch from torch's allocator (ordered by the stream it is made on)."""
     if workspace is None:
-        workspace = torch.empty(max(int(need), 16), dtype=torch.uint8, device=dev)
-    else:
-        _need_cuda_contig(workspace, "workspace")
+        need = need or 16
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    _need_cuda_contig(workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -277,7 +294,7 @@ def _grad_out(out, shape, dtype, accumulate, dev):
     if accumulate and out is None:
         raise ValueError("accumulate needs the sum to add to as out")
     if out is None:
-        return torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+        return torch.empty(*shape, dtype=dtype or torch.bfloat16, device=dev)
     _need_cuda_contig(out, "out")
     if tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must have shape {tuple(shape)}" + (f" and type {dtype}" if dtype else ""))
@@ -302,11 +319,16 @@ def weight_grad(dy, x: Act8, *, dtype=None, out=None, accumulate: bool = False, 
     if rows != st.rows:
         raise ValueError(f"dy and x must have the same rows, got {rows} and {st.rows}")
     dev = _one_dev(dy, x.q, x.scale, out, workspace)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         g = _grad_out(out, (M, st.cols), dtype, accumulate, dev)
         ws, nbytes = _scratch(workspace, lib.mc_weight_grad_workspace_size(rows, M, st.cols), dev)
         _check(lib.mc_weight_grad(dy.data_ptr(), ctypes.byref(st), M, g.data_ptr(), _dtype_code(g), int(bool(accumulate)),
                                   ws.data_ptr(), nbytes, s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return g
 
 
@@ -336,7 +358,9 @@ def expert_sort(idx, num_experts: int, *, workspace=None, stream=None) -> Expert
     T, K = int(idx.shape[0]), int(idx.shape[1])
     E = int(num_experts)
     dev = _one_dev(idx, workspace)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         # one allocation for the three results (each on a 16-byte boundary)
         n, o = -(-T * K // 4) * 4, -(-(max(E, 0) + 1) // 4) * 4
         buf = torch.empty(o + 2 * n, dtype=torch.int32, device=dev)
@@ -344,6 +368,9 @@ def expert_sort(idx, num_experts: int, *, workspace=None, stream=None) -> Expert
         ws, nbytes = _scratch(workspace, lib.mc_expert_sort_workspace_size(T, K, E), dev)
         _check(lib.mc_expert_sort(idx.data_ptr(), 64 if idx.dtype == torch.int64 else 32, T, K, E, plan.offsets.data_ptr(),
                                   plan.source.data_ptr(), plan.position.data_ptr(), ws.data_ptr(), nbytes, s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return plan
 
 
@@ -372,12 +399,17 @@ def expert_gather(x, plan: ExpertPlan, *, out=None, stream=None):
     _check_rows(x, "x", T)
     code, D = _dtype_code(x), int(x.shape[1])
     dev = _one_dev(x, plan.position, out)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         if out is None:
-            out = torch.empty((T * K, D), dtype=x.dtype, device=dev)
+            out = torch.empty(T * K, D, dtype=x.dtype, device=dev)
         else:
             _check_rows(out, "out", T * K, D, x.dtype)
         _check(lib.mc_expert_gather(x.data_ptr(), code, T, K, D, plan.position.data_ptr(), out.data_ptr(), s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return out
 
 
@@ -391,12 +423,17 @@ def expert_combine(y, plan: ExpertPlan, weights=None, *, out=None, stream=None):
         _check_weights(weights, T, K)
     code, D = _dtype_code(y), int(y.shape[1])
     dev = _one_dev(y, plan.position, weights, out)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         if out is None:
-            out = torch.empty((T, D), dtype=y.dtype, device=dev)
+            out = torch.empty(T, D, dtype=y.dtype, device=dev)
         else:
             _check_rows(out, "out", T, D, y.dtype)
         _check(lib.mc_expert_combine(y.data_ptr(), code, T, K, D, plan.position.data_ptr(), _ptr(weights), out.data_ptr(), s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return out
 
 
@@ -411,14 +448,19 @@ def expert_combine_backward(dout, y, plan: ExpertPlan, weights, *, out=None, str
     _check_rows(y, "y", T * K, D, dout.dtype)
     _check_weights(weights, T, K)
     dev = _one_dev(dout, y, plan.position, weights, out)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         if out is None:
-            out = torch.empty((T * K, D), dtype=y.dtype, device=dev)
+            out = torch.empty(T * K, D, dtype=y.dtype, device=dev)
         else:
             _check_rows(out, "out", T * K, D, y.dtype)
-        dw = torch.empty((T, K), dtype=torch.float32, device=dev)
+        dw = torch.empty(T, K, dtype=torch.float32, device=dev)
         _check(lib.mc_expert_combine_backward(dout.data_ptr(), y.data_ptr(), code, T, K, D, plan.position.data_ptr(),
                                               weights.data_ptr(), out.data_ptr(), dw.data_ptr(), s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return out, dw
 
 
@@ -438,10 +480,15 @@ def expert_weight_grad(dy, x: Act8, plan: ExpertPlan, *, gather: bool, dtype=Non
     if st.rows != (T if gather else rows):
         raise ValueError(f"x must have {T if gather else rows} rows, got {st.rows}")
     dev = _one_dev(dy, x.q, x.scale, plan.offsets, plan.position, out, workspace)
-    with _On(dev, stream) as s:
+    on = _enter(dev, stream)
+    try:
+        s = _raw_stream(dev.index)
         g = _grad_out(out, (E, M, st.cols), dtype, accumulate, dev)
         ws, nbytes = _scratch(workspace, lib.mc_expert_weight_grad_workspace_size(rows, E, M, st.cols), dev)
         _check(lib.mc_expert_weight_grad(dy.data_ptr(), rows, ctypes.byref(st), plan.offsets.data_ptr(),
                                          plan.position.data_ptr() if gather else None, K, E, M, g.data_ptr(), _dtype_code(g),
                                          int(bool(accumulate)), ws.data_ptr(), nbytes, s))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return g

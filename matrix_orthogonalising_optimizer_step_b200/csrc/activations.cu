@@ -275,9 +275,9 @@ int act_device_state(DeviceState** out) {
     const int gemm_smem = static_cast<int>(WGRAD_SMEM_BYTES);
     MC_CUDA(cudaFuncSetAttribute(weight_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem));
     MC_CUDA(cudaFuncSetAttribute(weight_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem));
-    const int sort_smem = (SORT_WARPS + 2) * (MAX_EXPERTS + 1) * 4;
-    MC_CUDA(cudaFuncSetAttribute(expert_place_kernel<int>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem));
-    MC_CUDA(cudaFuncSetAttribute(expert_place_kernel<long long>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem));
+    const int sort_smem = sort_place_smem<SORT_CLUSTER_THREADS>(MAX_EXPERTS);
+    MC_CUDA(cudaFuncSetAttribute(expert_place_kernel<int, SORT_CLUSTER_THREADS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem));
+    MC_CUDA(cudaFuncSetAttribute(expert_place_kernel<long long, SORT_CLUSTER_THREADS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, sort_smem));
     (*out)->act_init = true;
   }
   return MC_OK;
@@ -444,8 +444,34 @@ int check_move(int dtype, int64_t tokens, int top_k, int64_t cols) {
 }
 int64_t sort_tiles(int64_t pairs) { return (pairs + SORT_TILE - 1) / SORT_TILE; }
 
+// Blocks of the one-launch sort's cluster (a power of two), or 0 where it is not used.
+int sort_cluster(int64_t pairs) {
+  if (pairs <= SORT_TILE || pairs > SORT_CLUSTER_PAIRS) return 0;
+  int c = 1;
+  while (int64_t(c) * SORT_CLUSTER_TILE < pairs) c *= 2;
+  return c;
+}
+
 template <typename I>
 int sort_launch(const I* idx, int64_t pairs, int E, int* offsets, int* source, int* position, int* counts, cudaStream_t s) {
+  if (const int c = sort_cluster(pairs)) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(SORT_CLUSTER_THREADS);
+    cfg.dynamicSmemBytes = sort_place_smem<SORT_CLUSTER_THREADS>(E);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int* none = nullptr;
+    MC_CUDA(cudaLaunchKernelEx(&cfg, expert_place_kernel<I, SORT_CLUSTER_THREADS, true>, idx, none, none, offsets, source, position,
+                               static_cast<long long>(pairs), E));
+    return MC_OK;
+  }
   const unsigned tiles = static_cast<unsigned>(sort_tiles(pairs));
   int* totals = tiles > SORT_SCAN_TILES ? counts + size_t(tiles) * (E + 1) : nullptr;
   if (tiles > 1) {
@@ -456,7 +482,7 @@ int sort_launch(const I* idx, int64_t pairs, int E, int* offsets, int* source, i
     expert_scan_kernel<<<E + 1, SORT_THREADS, 0, s>>>(counts, totals, static_cast<int>(tiles), E + 1);
     MC_CUDA(cudaGetLastError());
   }
-  expert_place_kernel<I><<<tiles, SORT_THREADS, (SORT_WARPS + 2) * (E + 1) * sizeof(int), s>>>(
+  expert_place_kernel<I, SORT_THREADS, false><<<tiles, SORT_THREADS, sort_place_smem<SORT_THREADS>(E), s>>>(
       idx, tiles > 1 ? counts : nullptr, totals, offsets, source, position, pairs, E);
   MC_CUDA(cudaGetLastError());
   return MC_OK;
@@ -546,6 +572,7 @@ MC_API int mc_rms_norm(const void* x, const void* residual, const void* w, int d
   if ((rc = act_device_state(&st)) != MC_OK) return rc;
   const NormShape sh = norm_shape(rows, cols, st->sms);
   const unsigned blocks = static_cast<unsigned>((rows + sh.groups - 1) / sh.groups);
+  const dim3 dim(32 * sh.wpr, sh.groups);
   ProfScope prof(K_RMS_NORM, s, 0, 0, double(xb) * (residual ? 3 : 1) + double(n) * (y8 ? 1 + 1.0 / ACT_BLOCK : 2));
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
@@ -562,19 +589,19 @@ MC_API int mc_rms_norm(const void* x, const void* residual, const void* w, int d
     a.q_ld = y8 ? y8->q_ld : 0;
     a.s_ld = y8 ? y8->s_ld : 0;
     a.D = static_cast<int>(cols);
-    a.wpr = sh.wpr;
     a.w_f32 = w_dtype == MC_F32 ? 1 : 0;
     a.eps = eps;
+    a.inv_d = 1.0 / static_cast<double>(cols);
     with_fmt(y8 ? y8->fmt : -1, [&](auto f) {
       with_bool(cols % 8 == 0, [&](auto v) {
         constexpr int F = decltype(f)::value;
         constexpr bool V = decltype(v)::value;
         if (sh.threads <= 256) {
-          with_nv(sh.nv, [&](auto nv) { rms_norm_kernel<T, F, V, decltype(nv)::value, 256><<<blocks, sh.threads, 0, s>>>(a); });
+          with_nv(sh.nv, [&](auto nv) { rms_norm_kernel<T, F, V, decltype(nv)::value, 256><<<blocks, dim, 0, s>>>(a); });
         } else if (sh.nv == 1) {
-          rms_norm_kernel<T, F, V, 1, NORM_MAX_THREADS><<<blocks, sh.threads, 0, s>>>(a);
+          rms_norm_kernel<T, F, V, 1, NORM_MAX_THREADS><<<blocks, dim, 0, s>>>(a);
         } else {
-          rms_norm_kernel<T, F, V, 4, NORM_MAX_THREADS><<<blocks, sh.threads, 0, s>>>(a);
+          rms_norm_kernel<T, F, V, 4, NORM_MAX_THREADS><<<blocks, dim, 0, s>>>(a);
         }
       });
     });
@@ -695,9 +722,15 @@ MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, c
   MC_CUDA(err);
   MC_CUDA(cudaGetLastError());
   ProfScope prof(K_RMS_NORM_DW, s, 0, 0, 4.0 * parts * double(cols));
-  rms_norm_dw_kernel<<<static_cast<unsigned>((cols + 31) / 32), NORM_DW_WARPS * 32, 0, s>>>(static_cast<const float*>(workspace), dw,
-                                                                                          parts, static_cast<int>(cols));
-  MC_CUDA(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  set_pdl(attr[0], true);
+  cfg.gridDim = dim3(static_cast<unsigned>((cols + 31) / 32));
+  cfg.blockDim = dim3(NORM_DW_WARPS * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MC_CUDA(cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel, static_cast<const float*>(workspace), dw, parts, static_cast<int>(cols)));
   return MC_OK;
 }
 
@@ -756,7 +789,7 @@ MC_API int mc_expert_weight_grad(const void* dy, int64_t rows, const mc_act8* x,
 MC_API size_t mc_expert_sort_workspace_size(int64_t tokens, int top_k, int experts) {
   if (tokens < 0 || top_k < 1 || top_k > MAX_EXPERTS || tokens > kMaxRows / top_k || experts < 1 || experts > MAX_EXPERTS) return 0;
   const int64_t tiles = sort_tiles(tokens * top_k);
-  return align_up(tiles > 1 ? size_t(tiles + 1) * (experts + 1) * sizeof(int) : 16, 256);
+  return align_up(tiles > 1 && !sort_cluster(tokens * top_k) ? size_t(tiles + 1) * (experts + 1) * sizeof(int) : 16, 256);
 }
 
 MC_API int mc_expert_sort(const void* idx, int idx_bits, int64_t tokens, int top_k, int experts, int32_t* offsets,

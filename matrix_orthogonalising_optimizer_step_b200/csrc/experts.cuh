@@ -84,25 +84,46 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_scan_kernel(int* __restri
 
 // Places one tile's pairs.  A warp ranks 32 pairs at a time among equal
 // experts (match), over its own run of the tile; the warps' counts and the
-// other tiles' counts then give each (warp, expert) its first row.
-// `counts` null: there is one tile, and no counting launch.  `totals` given:
-// counts hold the sums over the tiles before, else every block adds them up
-// itself (up to SORT_SCAN_TILES tiles, where that costs less than a launch).
-template <typename I>
-__global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const I* __restrict__ idx, const int* __restrict__ counts,
-                                                                    const int* __restrict__ totals,
-                                                                    int* __restrict__ offsets, int* __restrict__ source,
-                                                                    int* __restrict__ position, long long pairs, int E) {
+// other tiles' counts then give each (warp, expert) its first row.  The other
+// tiles' counts come from
+//   CLUSTER  the blocks of this cluster, one tile each, through distributed
+//            shared memory: the whole sort is one launch (up to
+//            SORT_CLUSTER_PAIRS pairs; 32768 pairs for 64 experts took 18 us
+//            as a counting and a placing launch);
+//   counts   the counting launch.  `totals` given: counts hold the sums over the
+//            tiles before, else every block adds them up itself (up to
+//            SORT_SCAN_TILES tiles, where that costs less than a launch);
+//   neither  there is one tile.
+constexpr int SORT_CLUSTER_THREADS = 512;
+constexpr int SORT_CLUSTER_TILE = SORT_CLUSTER_THREADS * SORT_STEPS;
+constexpr int SORT_CLUSTER_PAIRS = 8 * SORT_CLUSTER_TILE;
+
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+template <int THREADS>
+__host__ __device__ constexpr int sort_place_smem(int E) { return (THREADS / 32 + 3) * (E + 1) * 4; }
+
+template <typename I, int THREADS, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS) expert_place_kernel(const I* __restrict__ idx, const int* __restrict__ counts,
+                                                               const int* __restrict__ totals, int* __restrict__ offsets,
+                                                               int* __restrict__ source, int* __restrict__ position,
+                                                               long long pairs, int E) {
   extern __shared__ int sort_smem[];
-  int* hist = sort_smem;                             // [SORT_WARPS][E + 1], then first rows
-  int* total = sort_smem + SORT_WARPS * (E + 1);     // [E + 1] pairs of each expert, then their exclusive sums
-  int* before = total + (E + 1);                     // [E + 1] of them in earlier tiles
-  __shared__ int warp_sum[SORT_WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int WARPS = THREADS / 32;
   const int n = E + 1;
-  for (int i = threadIdx.x; i < SORT_WARPS * n; i += SORT_THREADS) hist[i] = 0;
+  int* hist = sort_smem;              // [WARPS][n], then first rows
+  int* total = hist + WARPS * n;      // [n] pairs of each expert, in all
+  int* before = total + n;            // [n] of them in earlier tiles
+  int* local = before + n;            // [n] of them in this tile (CLUSTER)
+  __shared__ int warp_sum[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < WARPS * n; i += THREADS) hist[i] = 0;
   __syncthreads();
-  const long long base = (long long)blockIdx.x * SORT_TILE + warp * (32 * SORT_STEPS);
+  const long long base = (long long)blockIdx.x * (THREADS * SORT_STEPS) + warp * (32 * SORT_STEPS);
   int key[SORT_STEPS], rank[SORT_STEPS];
 #pragma unroll
   for (int i = 0; i < SORT_STEPS; ++i) key[i] = sort_key(idx, base + 32 * i + lane, pairs, E);
@@ -118,10 +139,24 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const I* __r
     rank[i] = had + below;
   }
   __syncthreads();
+  if constexpr (CLUSTER) {
+    for (int e = threadIdx.x; e < n; e += THREADS) {
+      int c = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) c += hist[w * n + e];
+      local[e] = c;
+    }
+    cluster_sync();
+  }
   // pairs per expert: of every tile, and of those before this one
-  for (int e = threadIdx.x; e < n; e += SORT_THREADS) {
+  for (int e = threadIdx.x; e < n; e += THREADS) {
     int all = 0, mine = 0;
-    if (totals) {
+    if constexpr (CLUSTER) {
+      for (unsigned t = 0; t < gridDim.x; ++t) {
+        if (t == blockIdx.x) mine = all;
+        all += ld_cluster(local + e, t);
+      }
+    } else if (totals) {
       all = totals[e];
       mine = counts[(long long)blockIdx.x * n + e];
     } else if (counts) {
@@ -130,15 +165,20 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const I* __r
         all += counts[(long long)t * n + e];
       }
     } else {
-      for (int w = 0; w < SORT_WARPS; ++w) all += hist[w * n + e];
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) all += hist[w * n + e];
     }
     total[e] = all;
     before[e] = mine;
   }
-  __syncthreads();
-  // exclusive sums over the experts, SORT_THREADS at a time
+  if constexpr (CLUSTER) {
+    cluster_sync();  // every block has read this one's counts
+  } else {
+    __syncthreads();
+  }
+  // exclusive sums over the experts, THREADS at a time
   int carry = 0;
-  for (int e0 = 0; e0 < n; e0 += SORT_THREADS) {
+  for (int e0 = 0; e0 < n; e0 += THREADS) {
     const int e = e0 + threadIdx.x;
     const int c = e < n ? total[e] : 0;
     int s = c;
@@ -151,7 +191,7 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const I* __r
     __syncthreads();
     int add = carry, chunk = 0;
 #pragma unroll
-    for (int w = 0; w < SORT_WARPS; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) add += warp_sum[w];
       chunk += warp_sum[w];
     }
@@ -159,7 +199,8 @@ __global__ void __launch_bounds__(SORT_THREADS) expert_place_kernel(const I* __r
       const int first = add + s - c;
       if (blockIdx.x == 0) offsets[e] = first;  // offsets[E] = rows in all (the dropped ones come behind)
       int row = first + before[e];
-      for (int w = 0; w < SORT_WARPS; ++w) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
         const int h = hist[w * n + e];
         hist[w * n + e] = row;
         row += h;

@@ -20,16 +20,15 @@ namespace mc {
 constexpr int NORM_MAX_THREADS = 1024;
 constexpr int NORM_MAX_COLS = 32768;  // 1024 threads x 4 fragments x 8 columns
 
-// Sum over the `wpr` warps that share a row; every thread of the block calls it.
+// Sum over the `wpr` warps that share a row, warps w0.. of the block, of which
+// this is the wr-th; every thread of the block calls it.
 template <typename F>
-__device__ __forceinline__ F row_sum(F v, int wpr, F* buf) {
+__device__ __forceinline__ F row_sum(F v, int wpr, int w0, int wr, F* buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (wpr == 1) return v;
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) buf[warp] = v;
+  if ((threadIdx.x & 31) == 0) buf[w0 + wr] = v;
   __syncthreads();
-  const int w0 = warp / wpr * wpr;
   F t = 0;
   for (int i = 0; i < wpr; ++i) t += buf[w0 + i];
   return t;
@@ -46,19 +45,15 @@ __device__ __forceinline__ double rsqrt64(double m) {
 }
 
 // x * r * w for an 8-bit output, as fp32 rounded to odd: r is given as
-// r_hi + r_lo, the product is kept to about 2^-46, and a result that is not
-// exact is moved to the neighbour with an odd last bit.  A rounding to 8 bits
-// of it is the rounding of the exact product (a value just beside the middle
-// of two codes never looks like the middle), so the codes are those of the
-// formula wherever the row's sum is.  Infinities and NaN pass through.
+// r_hi + r_lo, the product is kept to about 2^-46, cut toward zero and given an
+// odd last bit.  A rounding to 8 bits of it is then the rounding of the product
+// itself: a value just beside the middle of two codes never looks like the
+// middle (one exactly there, which takes an r of few bits, goes away from zero).
+// Infinities become NaN, which stands for the same in 8 bits.
 __device__ __forceinline__ float scaled_to_odd(float x, float w, float r_hi, float r_lo) {
   const float t_hi = r_hi * w;
   const float t_lo = fmaf(r_lo, w, fmaf(r_hi, w, -t_hi));
-  const float y = x * t_hi;
-  const float e = fmaf(x, t_lo, fmaf(x, t_hi, -y));
-  const int bits = __float_as_int(y);
-  const int toward = ((bits ^ __float_as_int(e)) >> 31) | 1;  // +1: the exact product is larger in magnitude
-  return __int_as_float(bits + ((fabsf(e) > 0.f && (bits & 1) == 0) ? toward : 0));
+  return __int_as_float(__float_as_int(__fmaf_rz(x, t_hi, x * t_lo)) | 1);
 }
 
 // The norm's weight of one fragment (bf16 or fp32), 0 past D.
@@ -86,31 +81,31 @@ struct NormFwdArgs {
   uint8_t* s;
   float* rstd;
   long long rows, q_ld, s_ld;
-  int D, wpr, w_f32;
+  int D, w_f32;
   float eps;
+  double inv_d;        // 1 / D
 };
 
-// The sum of squares is kept in 64 bits (an fp32 square is exact there): its
-// error would move every value of the row the same way.  B200 adds at half the
-// fp32 rate there, and the memory leaves room for it.
+// The sum of squares is kept in 64 bits beyond each fragment's eight terms: its
+// error would move every value of the row the same way.  (Every square in 64
+// bits: 115 us for 16384 x 4096 bf16 rows, bound by the conversions.)
 template <typename T, int FMT, bool VEC, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormFwdArgs<T> a) {
   __shared__ double buf[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = (blockDim.x >> 5) / a.wpr;
-  const long long row = (long long)blockIdx.x * groups + warp / a.wpr;
-  const int wr = warp % a.wpr;
+  // blockDim: {32 * warps of a row, rows}
+  const int lane = threadIdx.x & 31, wr = threadIdx.x >> 5, wpr = blockDim.x >> 5;
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < a.rows;
   const long long base = row * a.D;
   RawFrag<T> f[NV];
   double sum = 0.0;
   if (live) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_frag<VEC>(f[j], a.x + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D);
+    for (int j = 0; j < NV; ++j) load_frag<VEC>(f[j], a.x + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
     if (a.r) {
       RawFrag<T> fr[NV];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) load_frag<VEC>(fr[j], a.r + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D);
+      for (int j = 0; j < NV; ++j) load_frag<VEC>(fr[j], a.r + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float v[8], t[8];
@@ -119,29 +114,28 @@ __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormFwdArgs<T> 
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += t[i];
         frag_round(f[j], v);  // the norm sees h as the next layers will: in the stored type
-        store_raw<VEC>(a.h + base, (j * a.wpr + wr) * WARP_COLS, lane, a.D, f[j]);
+        store_raw<VEC>(a.h + base, (j * wpr + wr) * WARP_COLS, lane, a.D, f[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float v[8];
       frag_floats(f[j], v);
+      float t = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double d = v[i];
-        sum = fma(d, d, sum);
-      }
+      for (int i = 0; i < 8; ++i) t = fmaf(v[i], v[i], t);
+      sum += static_cast<double>(t);
     }
   }
-  sum = row_sum(sum, a.wpr, buf);
+  sum = row_sum(sum, wpr, threadIdx.y * wpr, wr, buf);
   if (!live) return;
-  const double r64 = rsqrt64(sum / static_cast<double>(a.D) + static_cast<double>(a.eps));
+  const double r64 = rsqrt64(fma(sum, a.inv_d, static_cast<double>(a.eps)));
   const float rstd = static_cast<float>(r64);
   const float r_lo = static_cast<float>(r64 - static_cast<double>(rstd));
   if (wr == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c0 = (j * a.wpr + wr) * WARP_COLS;
+    const int c0 = (j * wpr + wr) * WARP_COLS;
     if (c0 >= a.D) break;
     float v[8], w[8];
     frag_floats(f[j], v);
@@ -200,6 +194,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
   const int group = warp / a.wpr, wr = warp % a.wpr;
   const long long step = (long long)gridDim.x * groups;
   const float inv_d = 1.f / static_cast<float>(a.D);
+  griddep_launch_dependents();  // the sum over the parts may get ready
   float dw[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -261,7 +256,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
       }
     }
     // two buffers in turn: a warp still reading one row's sums never meets the next row's writes
-    const float c = row_sum(dot, a.wpr, buf[flip]) * inv_d;
+    const float c = row_sum(dot, a.wpr, group * a.wpr, wr, buf[flip]) * inv_d;
     flip ^= 1;
     if (live) {
 #pragma unroll
@@ -351,6 +346,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm
     fence_mbar_init();
   }
   __syncthreads();
+  griddep_launch_dependents();  // the sum over the parts may get ready
   const long long step = (long long)gridDim.x * groups;
   if (warp == workers) {
     // ------------------------------------------------------------ producer
@@ -498,16 +494,21 @@ __global__ void __launch_bounds__(NORM_DW_WARPS * 32) rms_norm_dw_kernel(const f
   __shared__ float buf[NORM_DW_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
-  if (c < D) {
-    int p = warp;
-    for (; p + 3 * NORM_DW_WARPS < parts; p += 4 * NORM_DW_WARPS) {
+  griddep_wait();  // launched while the walk still runs
+  constexpr int AHEAD = 8;
+  float t[AHEAD];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) t[u] += partial[(long long)(p + u * NORM_DW_WARPS) * D + c];
+  for (int u = 0; u < AHEAD; ++u) t[u] = 0.f;
+  if (c < D) {
+    for (int p = warp; p < parts; p += AHEAD * NORM_DW_WARPS) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int r = p + u * NORM_DW_WARPS;
+        if (r < parts) t[u] += partial[(long long)r * D + c];
+      }
     }
-    for (; p < parts; p += NORM_DW_WARPS) t[0] += partial[(long long)p * D + c];
   }
-  buf[warp][lane] = (t[0] + t[1]) + (t[2] + t[3]);
+  buf[warp][lane] = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
   __syncthreads();
   if (warp == 0 && c < D) {
     float v = 0.f;

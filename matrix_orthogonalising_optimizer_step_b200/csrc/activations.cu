@@ -213,46 +213,48 @@ int check_norm(const void* w, int dtype, int w_dtype, int64_t rows, int64_t cols
 constexpr int kWgradChunkKb = 16;
 
 struct WgradPlan {
-  int64_t ldx, ldy, ldp;     // rows of the bf16 X, of dY, of a partial product
-  int ranges, kb_range;      // one weight: the contraction in ranges
+  int64_t ldx, ldy;          // rows of the bf16 X and of dY
+  int64_t tiles, split;      // one weight: tiles in all, those of them whose contraction is split
+  int ranges, kb_range;      // into so many ranges of so many k-blocks
   bool copy_dy;
   size_t off_x, off_dy, off_part, off_maps, off_ranges, total;
 };
 
-// The split of one weight's contraction.  Few tiles leave SM pairs idle, so
-// the contraction is cut into ranges whose partial products are joined in
-// order; more ranges cost a partial product each (written and read in fp32).
-// The estimate: a k-block of a tile takes about 0.3 us, a tile's last drain 3
-// us, the partial products move at 5 TB/s and the joining launch takes 3 us.
-int wgrad_ranges(int64_t rows, int64_t M, int64_t N, int pairs) {
-  const int64_t tiles = ((M + BM - 1) / BM) * ((N + MMA_N - 1) / MMA_N);
-  const int64_t kb = (rows + BK - 1) / BK;
-  double best = 0;
-  int pick = 1;
-  for (int r = 1; r <= 32 && r <= std::max<int64_t>(1, kb / 4); ++r) {
-    const int64_t waves = (tiles * r + pairs - 1) / pairs;
-    const double us = double(waves) * ((kb + r - 1) / r) * 0.3 + 3.0 + (r > 1 ? 3.0 + 8.0 * r * double(M) * N / 5e6 : 0.0);
-    if (r == 1 || us < best) {
-      best = us;
-      pick = r;
-    }
-  }
-  return pick;
-}
-
 // CTA pairs that the plan counts on; the launch takes what the device has.
 constexpr int kPlanPairs = 74;
+
+// The split of one weight's contraction: the tiles beyond the whole waves of
+// all pairs, each into r ranges, where that is estimated to take less time than
+// a partial wave does.  The estimate: a k-block of a tile takes about 0.32 us,
+// the joining launch 4 us, and a partial product of 256 KB is written and read
+// at 5 TB/s.
+void wgrad_split(int64_t rows, int64_t M, int64_t N, WgradPlan& p) {
+  p.tiles = ((M + BM - 1) / BM) * ((N + MMA_N - 1) / MMA_N);
+  const int64_t kb = (rows + BK - 1) / BK, rem = p.tiles % kPlanPairs;
+  p.split = 0;
+  p.ranges = 1;
+  p.kb_range = static_cast<int>(kb);
+  double best = double(kb) * 0.32;  // the partial wave
+  for (int64_t r = 2; rem > 0 && r <= 32 && r * 4 <= kb; ++r) {
+    const int64_t per = (kb + r - 1) / r, used = (kb + per - 1) / per;  // none of the ranges empty
+    const int64_t waves = (rem * used + kPlanPairs - 1) / kPlanPairs;
+    const double us = double(waves) * per * 0.32 + 4.0 + double(rem * used) * (2.0 * BM * MMA_N * 4) / 5e6;
+    if (us < best) {
+      best = us;
+      p.split = rem;
+      p.ranges = static_cast<int>(used);
+      p.kb_range = static_cast<int>(per);
+    }
+  }
+}
 
 WgradPlan wgrad_plan(int64_t rows, int64_t M, int64_t N, int experts) {
   WgradPlan p;
   p.ldx = round8(N);
   p.copy_dy = M % 8 != 0;
   p.ldy = round8(M);
-  p.ldp = (N + 3) / 4 * 4;
-  p.ranges = experts > 0 ? 1 : wgrad_ranges(rows, M, N, kPlanPairs);
-  const int64_t kb = (rows + BK - 1) / BK;
-  p.kb_range = static_cast<int>((kb + p.ranges - 1) / p.ranges);
-  if (p.kb_range > 0) p.ranges = static_cast<int>((kb + p.kb_range - 1) / p.kb_range);  // none of them empty
+  wgrad_split(rows, M, N, p);
+  if (experts > 0) p.split = 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -261,7 +263,7 @@ WgradPlan wgrad_plan(int64_t rows, int64_t M, int64_t N, int experts) {
   };
   p.off_x = take(size_t(rows) * p.ldx * 2);
   p.off_dy = take(p.copy_dy ? size_t(rows) * p.ldy * 2 : 0);
-  p.off_part = take(p.ranges > 1 ? size_t(p.ranges) * M * p.ldp * 4 : 0);
+  p.off_part = take(size_t(p.split) * p.ranges * BM * MMA_N * 4);
   p.off_maps = take(size_t(experts) * 2 * sizeof(CUtensorMap));
   p.off_ranges = take(size_t(experts) * sizeof(int2));
   p.total = at + 256;  // the parts start at the first 256-byte boundary (tensor maps need 128)
@@ -348,7 +350,7 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
     wgrad_maps_kernel<<<experts, 32, 0, s>>>(mp);
     MC_CUDA(cudaGetLastError());
     P.maps = mp.maps;
-    P.ranges = mp.ranges;
+    P.ranges_of = mp.ranges;
   }
   // rows of the workspace are padded to whole 16 bytes, so this always takes the wide path
   if (position) {
@@ -367,47 +369,55 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
     return rc;
   }
 
-  const bool split = p.ranges > 1;
   P.M = static_cast<int>(M);
   P.N = static_cast<int>(N);
   P.kb_total = static_cast<int>((rows + BK - 1) / BK);
-  P.kb_range = p.kb_range;
-  P.out = split ? ws + p.off_part : g;
-  P.out_f32 = (split || g_dtype == MC_F32) ? 1 : 0;
-  P.add = (accumulate && !split) ? 1 : 0;
+  P.out = g;
+  P.out_f32 = g_dtype == MC_F32 ? 1 : 0;
+  P.add = accumulate ? 1 : 0;
   P.chunk_kb = P.out_f32 ? kWgradChunkKb : INT_MAX / 2;
   P.tiles_m = static_cast<int>((M + BM - 1) / BM);
   P.tiles_n = static_cast<int>((N + MMA_N - 1) / MMA_N);
   P.band = 8;
-  const int outs = split ? p.ranges : count;
-  const int64_t ldo = split ? p.ldp : N, es = P.out_f32 ? 4 : 2;
-  P.out_bs = M * ldo;
-  P.items = (long long)outs * P.tiles_m * P.tiles_n;
+  P.full_items = count * p.tiles - p.split;
+  P.items = P.full_items + p.split * p.ranges;
+  P.ranges = p.ranges;
+  P.kb_range = p.kb_range;
+  const int64_t es = dtype_bytes(g_dtype);
+  P.out_bs = M * N;
   P.err = st->err_ptr;
-  P.tma_out = (ldo * es) % 16 == 0 ? 1 : 0;
+  P.tma_out = (N * es) % 16 == 0 ? 1 : 0;
   if (P.tma_out) {
-    const uint64_t dims[3] = {uint64_t(N), uint64_t(M), uint64_t(outs)};
-    const uint64_t strides[2] = {uint64_t(ldo * es), uint64_t(ldo * es) * uint64_t(M)};
+    const uint64_t dims[3] = {uint64_t(N), uint64_t(M), uint64_t(count)};
+    const uint64_t strides[2] = {uint64_t(N * es), uint64_t(N * es) * uint64_t(M)};
     const uint32_t box[3] = {P.out_f32 ? 32u : 64u, 32, 1};
-    if ((rc = make_map(&P.map_o, P.out, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+    if ((rc = make_map(&P.map_o, g, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                        P.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != MC_OK)
       return rc;
   }
+  if (p.split) {
+    const uint64_t dims[3] = {uint64_t(MMA_N), uint64_t(BM), uint64_t(p.split) * p.ranges};
+    const uint64_t strides[2] = {uint64_t(MMA_N) * 4, uint64_t(MMA_N) * BM * 4};
+    const uint32_t box[3] = {32, 32, 1};
+    if ((rc = make_map(&P.map_p, ws + p.off_part, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_DATA_TYPE_FLOAT32)) != MC_OK)
+      return rc;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  set_pdl(attr[0], true);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.stream = s;
+  cfg.attrs = attr;
   {
     const double flops = 2.0 * double(rows) * M * N;
     ProfScope prof(K_WGRAD, s, flops, flops);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    set_pdl(attr[1], true);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(st->pair_clusters, P.items)));
     cfg.blockDim = dim3(GEMM_THREADS);
     cfg.dynamicSmemBytes = WGRAD_SMEM_BYTES;
-    cfg.stream = s;
-    cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (P.out_f32) {
       MC_CUDA(cudaLaunchKernelEx(&cfg, weight_grad_kernel<true>, P));
@@ -415,17 +425,21 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
       MC_CUDA(cudaLaunchKernelEx(&cfg, weight_grad_kernel<false>, P));
     }
   }
-  if (split) {
-    ProfScope prof(K_WGRAD_JOIN, s, 0, 0, double(M) * N * (4.0 * p.ranges + dtype_bytes(g_dtype)));
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((N + 1023) / 1024, 64)),
-                    static_cast<unsigned>(std::min<int64_t>(M, 16LL * st->sms)));
+  if (p.split) {
+    ProfScope prof(K_WGRAD_JOIN, s, 0, 0, double(p.split) * BM * MMA_N * (4.0 * p.ranges + es));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.split * (BM / JOIN_ROWS)));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
     const float* part = reinterpret_cast<const float*>(ws + p.off_part);
-    if (g_dtype == MC_F32) {
-      wgrad_join_kernel<float><<<grid, 256, 0, s>>>(part, static_cast<float*>(g), P.M, P.N, static_cast<int>(p.ldp), p.ranges, accumulate);
+    const int first = static_cast<int>(P.full_items);
+    if (P.out_f32) {
+      MC_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<float>, part, static_cast<float*>(g), P.M, P.N, P.tiles_m, P.tiles_n, P.band,
+                                 first, P.ranges, accumulate));
     } else {
-      wgrad_join_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(part, static_cast<__nv_bfloat16*>(g), P.M, P.N, static_cast<int>(p.ldp), p.ranges, 0);
+      MC_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<__nv_bfloat16>, part, static_cast<__nv_bfloat16*>(g), P.M, P.N, P.tiles_m,
+                                 P.tiles_n, P.band, first, P.ranges, 0));
     }
-    MC_CUDA(cudaGetLastError());
   }
   return MC_OK;
 }

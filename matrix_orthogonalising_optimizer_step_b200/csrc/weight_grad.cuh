@@ -24,6 +24,11 @@
 // gather (about 110 cycles per copy of 512 bytes) and 1.6 ms by 16-byte
 // asynchronous copies of four more warps.
 //
+// Tiles are dealt to the pairs in whole waves; the tiles of a last, partial
+// wave have their contraction split into `ranges`, whose fp32 partial products
+// go to scratch and are joined by one more launch, in order (4096 x 4096 from 8192
+// rows is 256 tiles for 74 pairs, 3.46 waves: see wgrad_plan for the figures).
+//
 // fp32 outputs: the tensor cores' own fp32 additions lose up to a unit in the
 // last place per step, always toward zero, so an accumulator takes at most
 // `chunk_kb` k-blocks; the epilogue threads add the chunks in registers, rounding
@@ -37,14 +42,17 @@ namespace mc {
 struct WgradParams {
   CUtensorMap map_a, map_b;   // one weight: dY [K][M] and X [K][N], boxes {64, 64}
   CUtensorMap map_o;          // output [count][M][N]: boxes of 32 rows x 128 bytes
+  CUtensorMap map_p;          // partial products [split items][256][256] fp32: boxes of 32 x 32
   const CUtensorMap* maps;    // experts: [2 * count] maps of dY's and X's rows of each, else null
-  const int2* ranges;         // experts: {first row, rows} of each
+  const int2* ranges_of;      // experts: {first row, rows} of each
   void* out;
   long long out_bs;           // elements from one problem's output to the next
-  long long items;            // count * tiles_m * tiles_n
+  long long items;            // work items: whole tiles, then the ranges of the split ones
+  long long full_items;       // count * tiles_m * tiles_n less the split tiles
+  int ranges;                 // one weight: ranges of each split tile
+  int kb_range;               // and their k-blocks
   int M, N;
   int kb_total;               // one weight: k-blocks of the whole contraction
-  int kb_range;               // and of each of the `count` ranges that it is split into
   int chunk_kb;
   int tiles_m, tiles_n, band;
   int out_f32, add, tma_out;
@@ -121,57 +129,76 @@ __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ 
 struct WgradItem {
   int prob, tm, tn;
   int kb_first, num_kb;
+  int part;  // index of the partial product, -1: the tile's whole contraction
 };
+// Row and column of tile `tl` of one output, in bands of `band` tile columns.
+__host__ __device__ inline void wgrad_tile(int tl, int tiles_m, int tiles_n, int band, int& tm, int& tn) {
+  const int per_band = tiles_m * band;
+  const int b = tl / per_band, x = tl - b * per_band;
+  const int rem = tiles_n - b * band;
+  const int w = rem < band ? rem : band;
+  tm = x / w;
+  tn = b * band + x % w;
+}
 __device__ __forceinline__ WgradItem wgrad_item(const WgradParams& P, long long t) {
   WgradItem it;
-  const long long tiles = (long long)P.tiles_m * P.tiles_n;
-  it.prob = static_cast<int>(t / tiles);
-  const int tl = static_cast<int>(t - it.prob * tiles);
-  const int per_band = P.tiles_m * P.band;
-  const int b = tl / per_band, x = tl - b * per_band;
-  const int rem = P.tiles_n - b * P.band;
-  const int w = rem < P.band ? rem : P.band;
-  it.tm = x / w;
-  it.tn = b * P.band + x % w;
-  if (P.maps) {
-    it.kb_first = 0;
-    it.num_kb = (P.ranges[it.prob].y + BK - 1) / BK;
+  it.prob = 0;
+  it.kb_first = 0;
+  it.num_kb = P.kb_total;
+  it.part = -1;
+  int tl;
+  if (t < P.full_items) {
+    const int tiles = P.tiles_m * P.tiles_n;
+    if (P.maps) {
+      it.prob = static_cast<int>(t / tiles);
+      it.num_kb = (P.ranges_of[it.prob].y + BK - 1) / BK;
+    }
+    tl = static_cast<int>(t - (long long)it.prob * tiles);
   } else {
-    it.kb_first = it.prob * P.kb_range;
-    it.num_kb = max(min(P.kb_range, P.kb_total - it.kb_first), 0);
+    it.part = static_cast<int>(t - P.full_items);
+    const int i = it.part / P.ranges;
+    tl = static_cast<int>(P.full_items) + i;
+    it.kb_first = (it.part - i * P.ranges) * P.kb_range;
+    it.num_kb = min(P.kb_range, P.kb_total - it.kb_first);
   }
+  wgrad_tile(tl, P.tiles_m, P.tiles_n, P.band, it.tm, it.tn);
   return it;
 }
 
 constexpr size_t WGRAD_SMEM_BYTES = TileCfg<0>::SMEM_BYTES + size_t(NUM_EPI_WARPS) * EPI_BUF_BYTES;
 
-// One warp's 32 rows x 128 bytes of an accumulator to the output.  `adding`:
-// into what is there.  v: the columns of this lane's row.
+// One warp's 32 rows x 128 bytes (fp32 or bf16 columns, `v`: those of this lane's
+// row) through its buffer to a tensor; `adding`: to what is there.
+template <bool F32>
+__device__ __forceinline__ void wgrad_tma_out(const CUtensorMap* map, int c0, int r0, int c2, int lane, uint8_t* buf, const float* v,
+                                              bool adding) {
+  if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
+  __syncwarp();
+  uint32_t w[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = F32 ? __float_as_uint(v[i]) : pack_bf16x2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(buf + epi_swz(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (adding) {
+      tma_add_3d(map, smem_u32(buf), c0, r0, c2);
+    } else {
+      tma_store_3d(map, smem_u32(buf), c0, r0, c2);
+    }
+    bulk_commit_group();
+  }
+}
+// The same to the output, or element by element where its rows are not whole 16-byte words.
 template <bool F32>
 __device__ __forceinline__ void wgrad_store(const WgradParams& P, int prob, int r0, int c0, int lane, uint8_t* buf,
                                             const float* v, bool adding) {
   constexpr int COLS = F32 ? 32 : 64;
   if (P.tma_out) {
-    if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
-    __syncwarp();
-    uint32_t w[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = F32 ? __float_as_uint(v[i]) : pack_bf16x2(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<uint4*>(buf + epi_swz(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (adding) {
-        tma_add_3d(&P.map_o, smem_u32(buf), c0, r0, prob);
-      } else {
-        tma_store_3d(&P.map_o, smem_u32(buf), c0, r0, prob);
-      }
-      bulk_commit_group();
-    }
+    wgrad_tma_out<F32>(&P.map_o, c0, r0, prob, lane, buf, v, adding);
   } else if (r0 + lane < P.M) {
-    // rows that are not whole 16-byte words: element by element, each by one thread
     const long long at = prob * P.out_bs + (long long)(r0 + lane) * P.N + c0;
 #pragma unroll
     for (int j = 0; j < COLS; ++j) {
@@ -229,6 +256,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
       prefetch_tmap(&P.map_b);
     }
     if (P.tma_out) prefetch_tmap(&P.map_o);
+    if (P.items > P.full_items) prefetch_tmap(&P.map_p);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
@@ -418,7 +446,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
         if (ok && r0 < P.M) {
 #pragma unroll
           for (int cb = 0; cb < WCOLS; cb += COLS) {
-            if (cbase + cb < P.N) wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, sum + cb, P.add != 0);
+            if (cbase + cb >= P.N) continue;
+            if (it.part >= 0) {
+              wgrad_tma_out<true>(&P.map_p, half * WCOLS + cb, HALF * static_cast<int>(rank) + q * 32, it.part, lane, buf, sum + cb, false);
+            } else {
+              wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, sum + cb, P.add != 0);
+            }
           }
         }
       } else {
@@ -433,7 +466,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
             if (cbase + cb >= P.N) break;
             float v[COLS];
             tmem_ld64(t_row + cb, v);
-            wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
+            if (it.part >= 0) {
+              const int pr = HALF * static_cast<int>(rank) + q * 32, pc = half * WCOLS + cb;
+              wgrad_tma_out<true>(&P.map_p, pc, pr, it.part, lane, buf, v, false);
+              wgrad_tma_out<true>(&P.map_p, pc + 32, pr, it.part, lane, buf, v + 32, false);
+            } else {
+              wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
+            }
           }
         }
         tc_fence_before();
@@ -462,28 +501,44 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
 }
 
 // ---------------------------------------------------------- split contraction
-// G = (G +) sum of the ranges' partial products, ranges in order.
+// The split tiles of G: (G +) the sum of their ranges' partial products, in
+// order.  A block takes JOIN_ROWS rows of one tile, four columns a thread.
+constexpr int JOIN_ROWS = 16;
 template <typename T>
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict__ part, T* __restrict__ out, int M, int N,
-                                                         int ldp, int ranges, int add) {
-  const long long bs = (long long)M * ldp;
-  for (long long r = blockIdx.y; r < M; r += gridDim.y) {
-    for (int c = (blockIdx.x * 256 + threadIdx.x) * 4; c < N; c += gridDim.x * 1024) {
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int p = 0; p < ranges; ++p) {
-        const float4 v = *reinterpret_cast<const float4*>(part + p * bs + r * ldp + c);
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-      }
-      const float t[4] = {s.x, s.y, s.z, s.w};
-      T* o = out + r * N + c;
+                                                         int tiles_m, int tiles_n, int band, int first_tile, int ranges, int add) {
+  const int split = blockIdx.x / (BM / JOIN_ROWS), strip = blockIdx.x % (BM / JOIN_ROWS);
+  int tm, tn;
+  wgrad_tile(first_tile + split, tiles_m, tiles_n, band, tm, tn);
+  const int cc = (threadIdx.x & 63) * 4, c = tn * MMA_N + cc;
+  const float* p = part + (long long)split * ranges * (BM * MMA_N) + cc;
+  griddep_wait();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (c + i < N) {
-          if constexpr (sizeof(T) == 4) {
-            o[i] = add ? o[i] + t[i] : t[i];
-          } else {
-            o[i] = __float2bfloat16_rn(t[i]);
-          }
+  for (int i = 0; i < JOIN_ROWS; i += 4) {
+    const int rr = strip * JOIN_ROWS + i + (threadIdx.x >> 6), r = tm * BM + rr;
+    if (r >= M || c >= N) continue;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < ranges; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (long long)k * (BM * MMA_N) + rr * MMA_N);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    const float t[4] = {s.x, s.y, s.z, s.w};
+    T* o = out + (long long)r * N + c;
+    if (N % 4 == 0 && !add) {  // whole aligned words
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(o) = s;
+      } else {
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      }
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c + j < N) {
+        if constexpr (sizeof(T) == 4) {
+          o[j] = add ? o[j] + t[j] : t[j];
+        } else {
+          o[j] = __float2bfloat16_rn(t[j]);
         }
       }
     }

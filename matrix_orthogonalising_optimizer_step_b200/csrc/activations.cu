@@ -371,6 +371,7 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
 
   P.M = static_cast<int>(M);
   P.N = static_cast<int>(N);
+  P.rows = static_cast<int>(rows);
   P.kb_total = static_cast<int>((rows + BK - 1) / BK);
   P.out = g;
   P.out_f32 = g_dtype == MC_F32 ? 1 : 0;
@@ -379,8 +380,10 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
   P.tiles_m = static_cast<int>((M + BM - 1) / BM);
   P.tiles_n = static_cast<int>((N + MMA_N - 1) / MMA_N);
   P.band = 8;
-  P.full_items = count * p.tiles - p.split;
-  P.items = P.full_items + p.split * p.ranges;
+  const int64_t items = count * p.tiles - p.split + p.split * p.ranges;
+  if (items > INT32_MAX / 2) return fail(MC_ERR_INVAL, "the gradients have too many tiles of 256 x 256");
+  P.full_items = static_cast<int>(count * p.tiles - p.split);
+  P.items = static_cast<int>(items);
   P.ranges = p.ranges;
   P.kb_range = p.kb_range;
   const int64_t es = dtype_bytes(g_dtype);
@@ -415,7 +418,7 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
   {
     const double flops = 2.0 * double(rows) * M * N;
     ProfScope prof(K_WGRAD, s, flops, flops);
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(st->pair_clusters, P.items)));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(st->pair_clusters, P.items)));
     cfg.blockDim = dim3(GEMM_THREADS);
     cfg.dynamicSmemBytes = WGRAD_SMEM_BYTES;
     cfg.numAttrs = 2;
@@ -432,7 +435,7 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     const float* part = reinterpret_cast<const float*>(ws + p.off_part);
-    const int first = static_cast<int>(P.full_items);
+    const int first = P.full_items;
     if (P.out_f32) {
       MC_CUDA(cudaLaunchKernelEx(&cfg, wgrad_join_kernel<float>, part, static_cast<float*>(g), P.M, P.N, P.tiles_m, P.tiles_n, P.band,
                                  first, P.ranges, accumulate));

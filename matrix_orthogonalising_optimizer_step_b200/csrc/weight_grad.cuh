@@ -47,12 +47,12 @@ struct WgradParams {
   const int2* ranges_of;      // experts: {first row, rows} of each
   void* out;
   long long out_bs;           // elements from one problem's output to the next
-  long long items;            // work items: whole tiles, then the ranges of the split ones
-  long long full_items;       // count * tiles_m * tiles_n less the split tiles
+  int items;                  // work items: whole tiles, then the ranges of the split ones
+  int full_items;             // count * tiles_m * tiles_n less the split tiles
   int ranges;                 // one weight: ranges of each split tile
   int kb_range;               // and their k-blocks
   int M, N;
-  int kb_total;               // one weight: k-blocks of the whole contraction
+  int rows, kb_total;         // one weight: rows and k-blocks of the whole contraction
   int chunk_kb;
   int tiles_m, tiles_n, band;
   int out_f32, add, tma_out;
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ 
 struct WgradItem {
   int prob, tm, tn;
   int kb_first, num_kb;
+  int rows;  // of the contraction, from kb_first on
   int part;  // index of the partial product, -1: the tile's whole contraction
 };
 // Row and column of tile `tl` of one output, in bands of `band` tile columns.
@@ -140,26 +141,28 @@ __host__ __device__ inline void wgrad_tile(int tl, int tiles_m, int tiles_n, int
   tm = x / w;
   tn = b * band + x % w;
 }
-__device__ __forceinline__ WgradItem wgrad_item(const WgradParams& P, long long t) {
+__device__ __forceinline__ WgradItem wgrad_item(const WgradParams& P, int t) {
   WgradItem it;
   it.prob = 0;
   it.kb_first = 0;
   it.num_kb = P.kb_total;
+  it.rows = P.rows;
   it.part = -1;
-  int tl;
-  if (t < P.full_items) {
-    const int tiles = P.tiles_m * P.tiles_n;
-    if (P.maps) {
-      it.prob = static_cast<int>(t / tiles);
-      it.num_kb = (P.ranges_of[it.prob].y + BK - 1) / BK;
-    }
-    tl = static_cast<int>(t - (long long)it.prob * tiles);
-  } else {
-    it.part = static_cast<int>(t - P.full_items);
+  if (t >= P.items) return it;
+  int tl = t;
+  if (t >= P.full_items) {
+    it.part = t - P.full_items;
     const int i = it.part / P.ranges;
-    tl = static_cast<int>(P.full_items) + i;
+    tl = P.full_items + i;
     it.kb_first = (it.part - i * P.ranges) * P.kb_range;
     it.num_kb = min(P.kb_range, P.kb_total - it.kb_first);
+    it.rows = P.rows - it.kb_first * BK;
+  } else if (P.maps) {
+    const int tiles = P.tiles_m * P.tiles_n;
+    it.prob = t / tiles;
+    tl = t - it.prob * tiles;
+    it.rows = P.ranges_of[it.prob].y;
+    it.num_kb = (it.rows + BK - 1) / BK;
   }
   wgrad_tile(tl, P.tiles_m, P.tiles_n, P.band, it.tm, it.tn);
   return it;
@@ -268,8 +271,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
   const uint32_t tmem_base = *tmem_slot;
   griddep_launch_dependents();
   griddep_wait();
-  const long long first_item = blockIdx.x >> 1;
-  const long long item_step = gridDim.x >> 1;
+  const int first_item = blockIdx.x >> 1;
+  const int item_step = gridDim.x >> 1;
 
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
       uint32_t filled = 0, fill_parity = 0;
       bool ok = true;
       int mapped = -1;
-      for (long long t = first_item; ok && t < P.items; t += item_step) {
+            for (int t = first_item; ok && t < P.items; t += item_step) {
         const WgradItem it = wgrad_item(P, t);
         const CUtensorMap* ma = P.maps ? P.maps + 2 * it.prob : &P.map_a;
         const CUtensorMap* mb = P.maps ? P.maps + 2 * it.prob + 1 : &P.map_b;
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
       const uint32_t idesc = idesc_bf16_f32(BM, MMA_N, 1, 1);
       const uint64_t ad0 = smem_desc_sw128(s0, MN_BOX_BYTES, 1024);
       const uint64_t bd0 = smem_desc_sw128(s0 + A_STAGE_BYTES, MN_BOX_BYTES, 1024);
-      for (long long t = first_item; ok && t < P.items; t += item_step) {
+            for (int t = first_item; ok && t < P.items; t += item_step) {
         const WgradItem it = wgrad_item(P, t);
         for (int c0 = 0; ok && c0 < it.num_kb; c0 += P.chunk_kb) {
           const int c1 = min(c0 + P.chunk_kb, it.num_kb);
@@ -362,8 +365,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
             for (int j = 0; j < T::KPS; ++j) {
               if (j >= nk) break;
               const uint64_t soff = static_cast<uint64_t>((stage * STAGE_BYTES + j * T::KB_BYTES) >> 4);
+              const int left = it.rows - (kb0 + j) * BK;  // the last k-block: no products of its zeros
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk) {
+                if (kk * 16 >= left) break;
                 const uint64_t koff = soff + ((kk * 16u * 128u) >> 4);
                 umma_bf16_pair(d_tmem, ad0 + koff, bd0 + koff, idesc, ((kb0 - c0 + j) | kk) != 0);
               }
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (long long t = first_item; ok && t < P.items; t += item_step) {
+        for (int t = first_item; ok && t < P.items; t += item_step) {
       const WgradItem it = wgrad_item(P, t);
       const int r0 = it.tm * BM + HALF * static_cast<int>(rank) + q * 32;
       const int cbase = it.tn * T::N + half * WCOLS;
@@ -460,24 +465,24 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
         if (!__all_sync(0xffffffffu, got)) break;
         tc_fence_after();
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * T::N + half * WCOLS;
-        if (r0 < P.M) {
-#pragma unroll 1
-          for (int cb = 0; cb < WCOLS; cb += COLS) {
-            if (cbase + cb >= P.N) break;
-            float v[COLS];
-            tmem_ld64(t_row + cb, v);
-            if (it.part >= 0) {
-              const int pr = HALF * static_cast<int>(rank) + q * 32, pc = half * WCOLS + cb;
-              wgrad_tma_out<true>(&P.map_p, pc, pr, it.part, lane, buf, v, false);
-              wgrad_tma_out<true>(&P.map_p, pc + 32, pr, it.part, lane, buf, v + 32, false);
-            } else {
-              wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
-            }
+#pragma unroll
+        for (int cb = 0; cb < WCOLS; cb += COLS) {
+          float v[COLS];
+          tmem_ld64(t_row + cb, v);
+          if (cb + COLS == WCOLS) {  // the accumulator is in registers: the next tile may have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
+          }
+          if (r0 >= P.M || cbase + cb >= P.N) continue;
+          if (it.part >= 0) {
+            const int pr = HALF * static_cast<int>(rank) + q * 32, pc = half * WCOLS + cb;
+            wgrad_tma_out<true>(&P.map_p, pc, pr, it.part, lane, buf, v, false);
+            wgrad_tma_out<true>(&P.map_p, pc + 32, pr, it.part, lane, buf, v + 32, false);
+          } else {
+            wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
         if (++acc == NACC) {
           acc = 0;
           acc_phase ^= 1;

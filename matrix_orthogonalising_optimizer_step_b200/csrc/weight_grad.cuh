@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
       uint32_t filled = 0, fill_parity = 0;
       bool ok = true;
       int mapped = -1;
-            for (int t = first_item; ok && t < P.items; t += item_step) {
+      for (int t = first_item; ok && t < P.items; t += item_step) {
         const WgradItem it = wgrad_item(P, t);
         const CUtensorMap* ma = P.maps ? P.maps + 2 * it.prob : &P.map_a;
         const CUtensorMap* mb = P.maps ? P.maps + 2 * it.prob + 1 : &P.map_b;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
       const uint32_t idesc = idesc_bf16_f32(BM, MMA_N, 1, 1);
       const uint64_t ad0 = smem_desc_sw128(s0, MN_BOX_BYTES, 1024);
       const uint64_t bd0 = smem_desc_sw128(s0 + A_STAGE_BYTES, MN_BOX_BYTES, 1024);
-            for (int t = first_item; ok && t < P.items; t += item_step) {
+      for (int t = first_item; ok && t < P.items; t += item_step) {
         const WgradItem it = wgrad_item(P, t);
         for (int c0 = 0; ok && c0 < it.num_kb; c0 += P.chunk_kb) {
           const int c1 = min(c0 + P.chunk_kb, it.num_kb);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-        for (int t = first_item; ok && t < P.items; t += item_step) {
+    for (int t = first_item; ok && t < P.items; t += item_step) {
       const WgradItem it = wgrad_item(P, t);
       const int r0 = it.tm * BM + HALF * static_cast<int>(rank) + q * 32;
       const int cbase = it.tn * T::N + half * WCOLS;

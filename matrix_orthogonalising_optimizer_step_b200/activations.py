@@ -16,10 +16,11 @@ from typing import NamedTuple
 
 import torch
 
-from . import (McAct8, MC_ACT_E4M3, MC_ACT_INT8, _check, _dtype_code, _need_cuda_contig, _one_device, _ptr,
+from . import (MC_ACT_E4M3, MC_ACT_INT8, MC_BF16, MC_F32, McAct8, _check, _need_cuda_contig, _one_device, _ptr,
                load_library)
 
 ACT_BLOCK = 32
+_CODE = {torch.float32: MC_F32, torch.bfloat16: MC_BF16}
 _FMT = {"e4m3": MC_ACT_E4M3, "int8": MC_ACT_INT8}
 
 
@@ -72,11 +73,18 @@ def _enter(device, stream):
 
 def _one_dev(first, *others):
     """The device of ``first``; raises unless every other (non-None) tensor is on it."""
-    dev = first.device
+    at = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != at:
             _one_device([first, *others])
-    return dev
+    return first.device
+
+
+def _dtype_code(t):
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return code
 
 
 def _rows_cols(shape):
@@ -332,18 +340,21 @@ def weight_grad(dy, x: Act8, *, dtype=None, out=None, accumulate: bool = False, 
     return g
 
 
-def _check_plan(plan):
-    off, src, pos = plan
-    i32 = torch.int32
-    for t, nm in ((off, "offsets"), (src, "source"), (pos, "position")):
-        if not (t.is_cuda and t.is_contiguous()):
-            _need_cuda_contig(t, f"plan.{nm}")
-        if t.dtype is not i32:
-            raise TypeError(f"plan.{nm} must be int32")
+def _plan_part(t, name):
+    if not (t.is_cuda and t.is_contiguous()):
+        _need_cuda_contig(t, name)
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32")
+
+
+def _plan_pairs(plan):
+    """(T, K) of the plan's ``position``, which is all that moving rows goes by."""
+    pos = plan.position
+    _plan_part(pos, "plan.position")
     shape = pos.shape
-    if len(shape) != 2 or shape[1] < 1 or off.dim() != 1 or off.shape[0] < 2 or src.shape != (shape[0] * shape[1],):
-        raise ValueError("plan must hold offsets [E + 1], source [T * K] and position [T, K]")
-    return shape[0], shape[1], off.shape[0] - 1
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"plan.position must be 2D [T, K], got shape {tuple(shape)}")
+    return shape
 
 
 def expert_sort(idx, num_experts: int, *, workspace=None, stream=None) -> ExpertPlan:
@@ -376,7 +387,8 @@ def expert_sort(idx, num_experts: int, *, workspace=None, stream=None) -> Expert
 
 def _check_rows(t, name, rows, cols=None, dtype=None):
     _need_matrix(t, name)
-    if t.dim() != 2 or t.shape[0] != rows or (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} must have shape ({rows}, {'D' if cols is None else cols}), got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
@@ -386,7 +398,7 @@ def _check_weights(w, T, K):
     _need_cuda_contig(w, "weights")
     if w.dtype != torch.float32:
         raise TypeError("weights must be float32")
-    if tuple(w.shape) != (T, K):
+    if w.shape != (T, K):
         raise ValueError(f"weights must have shape {(T, K)}, got {tuple(w.shape)}")
 
 
@@ -395,9 +407,9 @@ def expert_gather(x, plan: ExpertPlan, *, out=None, stream=None):
     [T * K, D].  Rows behind the last expert's are left as they are in ``out``,
     unset otherwise.  Its gradient is ``expert_combine`` without weights."""
     lib = load_library()
-    T, K, _ = _check_plan(plan)
+    T, K = _plan_pairs(plan)
     _check_rows(x, "x", T)
-    code, D = _dtype_code(x), int(x.shape[1])
+    code, D = _dtype_code(x), x.shape[1]
     dev = _one_dev(x, plan.position, out)
     on = _enter(dev, stream)
     try:
@@ -417,11 +429,11 @@ def expert_combine(y, plan: ExpertPlan, weights=None, *, out=None, stream=None):
     """[T, D]: each token's sum of its pairs' rows of y [T * K, D], times
     weights [T, K] (fp32; none: ones), in fp32 and rounded once."""
     lib = load_library()
-    T, K, _ = _check_plan(plan)
+    T, K = _plan_pairs(plan)
     _check_rows(y, "y", T * K)
     if weights is not None:
         _check_weights(weights, T, K)
-    code, D = _dtype_code(y), int(y.shape[1])
+    code, D = _dtype_code(y), y.shape[1]
     dev = _one_dev(y, plan.position, weights, out)
     on = _enter(dev, stream)
     try:
@@ -442,9 +454,9 @@ def expert_combine_backward(dout, y, plan: ExpertPlan, weights, *, out=None, str
     Rows of dy behind the last expert's are left as they are in ``out``, unset
     otherwise; ``out`` may be y itself."""
     lib = load_library()
-    T, K, _ = _check_plan(plan)
+    T, K = _plan_pairs(plan)
     _check_rows(dout, "dout", T)
-    code, D = _dtype_code(dout), int(dout.shape[1])
+    code, D = _dtype_code(dout), dout.shape[1]
     _check_rows(y, "y", T * K, D, dout.dtype)
     _check_weights(weights, T, K)
     dev = _one_dev(dout, y, plan.position, weights, out)
@@ -471,7 +483,11 @@ def expert_weight_grad(dy, x: Act8, plan: ExpertPlan, *, gather: bool, dtype=Non
     x in 8 bits: in token order (``gather`` true: [T, in-features], e.g. the
     input of the experts' first products) or sorted like dy (``gather`` false)."""
     lib = load_library()
-    T, K, E = _check_plan(plan)
+    T, K = _plan_pairs(plan)
+    _plan_part(plan.offsets, "plan.offsets")
+    if plan.offsets.dim() != 1 or plan.offsets.shape[0] < 2:
+        raise ValueError(f"plan.offsets must be 1D [E + 1], got shape {tuple(plan.offsets.shape)}")
+    E = plan.offsets.shape[0] - 1
     _need_dy(dy)
     rows, M = _rows_cols(dy.shape)
     if rows != T * K:

@@ -127,14 +127,21 @@ __device__ __forceinline__ void store_frag(float* row, int c0, int lane, int D, 
   }
 }
 
-// Values rounded to the fragment's type, and the fragment as it is to memory.
-__device__ __forceinline__ void frag_round(RawFrag<__nv_bfloat16>& f, const float (&v)[8]) {
-  f.q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+// f + g, rounded to the type.  Two bf16 numbers: their sum is exact in fp32
+// unless they are so far apart (over 2^16) that it rounds to the larger one, so
+// one rounding and the detour over fp32 give the same.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
 }
-__device__ __forceinline__ void frag_round(RawFrag<float>& f, const float (&v)[8]) {
-  f.a = make_float4(v[0], v[1], v[2], v[3]);
-  f.b = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void frag_add(RawFrag<__nv_bfloat16>& f, const RawFrag<__nv_bfloat16>& g) {
+  f.q = make_uint4(add_bf16x2(f.q.x, g.q.x), add_bf16x2(f.q.y, g.q.y), add_bf16x2(f.q.z, g.q.z), add_bf16x2(f.q.w, g.q.w));
 }
+__device__ __forceinline__ void frag_add(RawFrag<float>& f, const RawFrag<float>& g) {
+  f.a = make_float4(f.a.x + g.a.x, f.a.y + g.a.y, f.a.z + g.a.z, f.a.w + g.a.w);
+  f.b = make_float4(f.b.x + g.b.x, f.b.y + g.b.y, f.b.z + g.b.z, f.b.w + g.b.w);
+}
+// The fragment as it is to memory.
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_raw(T* row, int c0, int lane, int D, const RawFrag<T>& f) {
   if constexpr (VEC && sizeof(T) == 2) {
@@ -333,6 +340,7 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
                                                                   long long rows, int D, long long q_ld,
                                                                   long long s_ld, long long out_ld, int chunks) {
   constexpr int UNROLL = 4;
+  griddep_launch_dependents();  // a weight gradient's product may set itself up
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
   const long long first = (long long)blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);
@@ -369,6 +377,7 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_scatter_kernel(const uint8_t
                                                                    int D, long long q_ld, long long s_ld, long long out_ld,
                                                                    int segments) {
   constexpr int RUNS = 4;  // 256-column runs of an item
+  griddep_launch_dependents();  // the product may set itself up
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
   const long long first = (long long)blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);

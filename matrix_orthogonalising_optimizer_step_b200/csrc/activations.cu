@@ -700,8 +700,12 @@ MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, c
         if (rs.wpr) {
           auto launch = [&](auto kernel, int per_sm) {
             const int smem = ring.stages * ring.stage_bytes;
-            if (smem > 40 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (err != cudaSuccess) return;
+            if (st->wide_smem.insert(reinterpret_cast<const void*>(kernel)).second)
+              err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytesWide);
+            if (err != cudaSuccess) {
+              st->wide_smem.erase(reinterpret_cast<const void*>(kernel));
+              return;
+            }
             const unsigned blocks = static_cast<unsigned>(
                 std::min<int64_t>((rows + rs.groups - 1) / rs.groups, std::min<int64_t>(kNormBwdBlocks, int64_t(per_sm) * st->sms)));
             parts = static_cast<int>(blocks) * rs.groups;

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <set>
 #include <string>
 #include <vector>
 
@@ -33,6 +34,7 @@ constexpr int kSmemOptIn = 232448;
 struct DeviceState {
   bool init = false;
   bool act_init = false;  // the activation operators' kernel attributes are set
+  std::set<const void*> wide_smem;  // kernels allowed more than 48 KiB of shared memory on first use
   int sms = 0;
   int pair_clusters = 0;  // CTA pairs of the GEMM kernel that fit on the device at once
   int cc_major = 0, cc_minor = 0;

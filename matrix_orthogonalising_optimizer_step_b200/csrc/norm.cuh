@@ -55,6 +55,10 @@ __device__ __forceinline__ float scaled_to_odd(float x, float w, float r_hi, flo
   const float t_lo = fmaf(r_lo, w, fmaf(r_hi, w, -t_hi));
   return __int_as_float(__float_as_int(__fmaf_rz(x, t_hi, x * t_lo)) | 1);
 }
+// The same where x * w is exact in fp32 (two bf16 numbers).
+__device__ __forceinline__ float scaled_to_odd(float xw, float r_hi, float r_lo) {
+  return __int_as_float(__float_as_int(__fmaf_rz(xw, r_hi, xw * r_lo)) | 1);
+}
 
 // The norm's weight of one fragment (bf16 or fp32), 0 past D.
 template <bool VEC>
@@ -108,12 +112,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormFwdArgs<T> 
       for (int j = 0; j < NV; ++j) load_frag<VEC>(fr[j], a.r + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        float v[8], t[8];
-        frag_floats(f[j], v);
-        frag_floats(fr[j], t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += t[i];
-        frag_round(f[j], v);  // the norm sees h as the next layers will: in the stored type
+        frag_add(f[j], fr[j]);  // the norm sees h as the next layers will: in the stored type
         store_raw<VEC>(a.h + base, (j * wpr + wr) * WARP_COLS, lane, a.D, f[j]);
       }
     }
@@ -146,8 +145,13 @@ __global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormFwdArgs<T> 
       for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * w[i];
       store_frag<VEC>(a.y + base, c0, lane, a.D, v);
     } else {
+      if (sizeof(T) == 2 && !a.w_f32) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i], w[i], rstd, r_lo);
+        for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i] * w[i], rstd, r_lo);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i], w[i], rstd, r_lo);
+      }
       store_frag8<FMT, VEC>(a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D, v);
     }
   }

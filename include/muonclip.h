@@ -494,8 +494,8 @@ typedef struct {
   void* scale;      /* device, rows x s_ld bytes, 16-byte aligned */
   int64_t rows;     /* >= 0 */
   int64_t cols;     /* >= 1 */
-  int64_t q_ld;     /* multiple of 16, >= cols */
-  int64_t s_ld;     /* multiple of 16, >= ceil(cols / 32) */
+  int64_t q_ld;     /* multiple of 16, >= cols, at most 2^30 */
+  int64_t s_ld;     /* multiple of 16, >= ceil(cols / 32), at most 2^30 */
   int32_t fmt;      /* MC_ACT_E4M3 or MC_ACT_INT8 */
   int32_t reserved;
 } mc_act8;

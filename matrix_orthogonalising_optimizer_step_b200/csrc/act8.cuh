@@ -221,18 +221,24 @@ __device__ __forceinline__ void store_frag8(uint8_t* qrow, uint8_t* srow, int c0
       if ((lane & 3) == 0) srow[c / ACT_BLOCK] = fine ? static_cast<uint8_t>(k + 127) : 255;
     }
   } else {
-    uint32_t mine = 0;  // lane i keeps block i's scale byte
+    // lane i (mod 8) works out block i's scale, for all lanes
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      const bool fine = m < 0x7F800000u;
-      const int k = act_exponent<FMT>(m);
-      const uint32_t code = act_encode2<FMT>(v[i] * exp2_int(-k), 0.f) & 0xFFu;
-      const int c = c0 + 32 * i + lane;
-      if (c < D) qrow[c] = fine ? static_cast<uint8_t>(code) : 0;
-      if (lane == i) mine = fine ? static_cast<uint32_t>(k + 127) : 255u;
+      const uint32_t mi = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      if ((lane & 7) == i) m = mi;
     }
-    if (lane < 8 && c0 + 32 * lane < D) srow[c0 / ACT_BLOCK + lane] = static_cast<uint8_t>(mine);
+    const bool fine = m < 0x7F800000u;
+    const int k = act_exponent<FMT>(m);
+    const float r = fine ? exp2_int(-k) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float ri = __shfl_sync(0xffffffffu, r, i);
+      const uint32_t code = act_encode2<FMT>(v[i] * ri, 0.f);
+      const int c = c0 + 32 * i + lane;
+      if (c < D) qrow[c] = ri > 0.f ? static_cast<uint8_t>(code) : 0;
+    }
+    if (lane < 8 && c0 + 32 * lane < D) srow[c0 / ACT_BLOCK + lane] = fine ? static_cast<uint8_t>(k + 127) : 255;
   }
 }
 

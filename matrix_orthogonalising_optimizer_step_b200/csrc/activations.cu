@@ -45,7 +45,7 @@ int check_act8(const mc_act8* a) {
   if (a->q_ld < a->cols || a->q_ld % 16 != 0) return fail(MC_ERR_INVAL, "mc_act8: q_ld must be a multiple of 16, at least cols");
   if (a->s_ld < (a->cols + ACT_BLOCK - 1) / ACT_BLOCK || a->s_ld % 16 != 0)
     return fail(MC_ERR_INVAL, "mc_act8: s_ld must be a multiple of 16, at least one byte per 32 columns");
-  if (a->q_ld > (int64_t(1) << 32) || a->s_ld > (int64_t(1) << 32)) return fail(MC_ERR_INVAL, "mc_act8: row strides too large");
+  if (a->q_ld > (int64_t(1) << 30) || a->s_ld > (int64_t(1) << 30)) return fail(MC_ERR_INVAL, "mc_act8: row strides too large");
   if (a->rows > 0 && (!a->q || !a->scale)) return fail(MC_ERR_INVAL, "mc_act8: NULL q or scale");
   if (!aligned16(a->q) || !aligned16(a->scale)) return fail(MC_ERR_ALIGN, "mc_act8: q and scale must be 16-byte aligned");
   return MC_OK;
@@ -145,8 +145,8 @@ NormShape norm_bwd_shape(int64_t cols) {
 constexpr int kNormBwdBlocks = 640;  // most blocks of the gradient's walk
 
 // The gradient through the shared-memory ring.  wpr = 0: the row does not fit.
-constexpr int kNormRingBytes = 100 * 1024;      // of a block of 8 warps: two of them share an SM
-constexpr int kNormRingBytesWide = 200 * 1024;  // of a block of up to 16
+constexpr int kNormRingBytes = 100 * 1024;      // of a block that shares an SM with another
+constexpr int kNormRingBytesWide = 200 * 1024;  // of a block that has an SM to itself
 NormShape norm_ring_shape(int64_t cols, int64_t row_bytes, int64_t q_row, int64_t s_row, bool dh, NormRing* R) {
   const int frags = static_cast<int>((cols + WARP_COLS - 1) / WARP_COLS);
   NormShape n;
@@ -158,7 +158,8 @@ NormShape norm_ring_shape(int64_t cols, int64_t row_bytes, int64_t q_row, int64_
   const int64_t rows_b = at(n.groups * row_bytes);
   const int64_t h_b = q_row ? at(n.groups * q_row) + at(n.groups * s_row) : rows_b;
   const int64_t stage = rows_b * (dh ? 2 : 1) + h_b;
-  const int64_t room = n.wpr <= 8 ? kNormRingBytes : kNormRingBytesWide;
+  // two blocks an SM where two stages of either fit, else one
+  const int64_t room = n.wpr <= 8 && 2 * stage <= kNormRingBytes ? kNormRingBytes : kNormRingBytesWide;
   const int64_t stages = std::min<int64_t>(NORM_RING_STAGES, room / stage);
   if (n.wpr > 16 || stages < 2) {
     n.wpr = 0;
@@ -323,9 +324,8 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
   const void* a = dy;
   if (p.copy_dy) {
     ProfScope prof(K_WGRAD_PREP, s, 0, 0, 4.0 * double(rows) * M);
-    wgrad_copy_kernel<<<static_cast<unsigned>(std::min<int64_t>(rows, 16LL * st->sms)), 256, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(dy), reinterpret_cast<__nv_bfloat16*>(ws + p.off_dy), rows, static_cast<int>(M),
-        static_cast<int>(p.ldy));
+    wgrad_copy_kernel<<<static_cast<unsigned>(std::min<int64_t>(rows, 32LL * st->sms)), 256, 0, s>>>(
+        static_cast<const uint16_t*>(dy), reinterpret_cast<uint32_t*>(ws + p.off_dy), rows, static_cast<int>(M), static_cast<int>(p.ldy));
     MC_CUDA(cudaGetLastError());
     a = ws + p.off_dy;
   }
@@ -560,13 +560,13 @@ MC_API int mc_rms_norm(const void* x, const void* residual, const void* w, int d
   int rc = check_norm(w, dtype, w_dtype, rows, cols);
   if (rc != MC_OK) return rc;
   if (!(eps >= 0.f) || eps > 1e30f) return fail(MC_ERR_INVAL, "eps must be finite and not negative");
+  if (rows == 0) return MC_OK;
   if ((y_out != nullptr) == (y8 != nullptr)) return fail(MC_ERR_INVAL, "exactly one of y_out and y8 must be given");
   if (y8) {
     if ((rc = check_act8(y8)) != MC_OK) return rc;
     if (y8->rows != rows || y8->cols != cols) return fail(MC_ERR_INVAL, "y8 must have the shape of x");
   }
   if ((residual != nullptr) != (h_out != nullptr)) return fail(MC_ERR_INVAL, "h_out goes with residual, and residual with h_out");
-  if (rows == 0) return MC_OK;
   if (!x || !rstd_out) return fail(MC_ERR_INVAL, "NULL x or rstd_out");
   if (!aligned16(x) || !aligned16(residual) || !aligned16(h_out) || !aligned16(y_out) || !aligned16(rstd_out))
     return fail(MC_ERR_ALIGN, "pointers must be 16-byte aligned");
@@ -719,24 +719,23 @@ MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, c
           }
           return;
         }
-        with_bool(cols % 8 == 0, [&](auto v) {
-          auto launch = [&](auto kernel) {
-            int per_sm = 0;
-            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, sh.threads, 0);
-            if (err != cudaSuccess) return;
-            const int64_t most = std::min<int64_t>(kNormBwdBlocks, int64_t(std::max(per_sm, 1)) * st->sms);
-            const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((rows + sh.groups - 1) / sh.groups, most));
-            parts = static_cast<int>(blocks) * sh.groups;
-            kernel<<<blocks, sh.threads, 0, s>>>(a);
-          };
-          constexpr int F = decltype(f)::value;
-          constexpr bool V = decltype(v)::value;
-          if (sh.threads > 256) {
-            launch(rms_norm_bwd_kernel<T, F, V, 4, NORM_MAX_THREADS>);
-          } else {
-            with_nv(sh.nv, [&](auto nv) { launch(rms_norm_bwd_kernel<T, F, V, decltype(nv)::value, 256>); });
-          }
-        });
+        auto launch = [&](auto kernel) {
+          int per_sm = 0;
+          err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, sh.threads, 0);
+          if (err != cudaSuccess) return;
+          const int64_t most = std::min<int64_t>(kNormBwdBlocks, int64_t(std::max(per_sm, 1)) * st->sms);
+          const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((rows + sh.groups - 1) / sh.groups, most));
+          parts = static_cast<int>(blocks) * sh.groups;
+          kernel<<<blocks, sh.threads, 0, s>>>(a);
+        };
+        constexpr int F = decltype(f)::value;
+        if (cols % 8 == 0) {  // rows too wide for the ring
+          launch(rms_norm_bwd_kernel<T, F, true, 4, NORM_MAX_THREADS>);
+        } else if (sh.threads > 256) {
+          launch(rms_norm_bwd_kernel<T, F, false, 4, NORM_MAX_THREADS>);
+        } else {
+          with_nv(sh.nv, [&](auto nv) { launch(rms_norm_bwd_kernel<T, F, false, decltype(nv)::value, 256>); });
+        }
       });
     });
   }

@@ -94,7 +94,7 @@ struct NormFwdArgs {
 // error would move every value of the row the same way.  (Every square in 64
 // bits: 115 us for 16384 x 4096 bf16 rows, bound by the conversions.)
 template <typename T, int FMT, bool VEC, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) rms_norm_kernel(const NormFwdArgs<T> a) {
+__global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<T> a) {
   __shared__ double buf[32];
   // blockDim: {32 * warps of a row, rows}
   const int lane = threadIdx.x & 31, wr = threadIdx.x >> 5, wpr = blockDim.x >> 5;
@@ -191,7 +191,7 @@ struct NormBwdRaw<T, ACT_INT8> {
 // registers; the next row's loads are issued before this row's sum, so that
 // the memory stays busy across the block-wide reduction.
 template <typename T, int FMT, bool VEC, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs<T> a) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs<T> a) {
   __shared__ float buf[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = (blockDim.x >> 5) / a.wpr;

@@ -194,27 +194,49 @@ __device__ __forceinline__ void wgrad_tma_out(const CUtensorMap* map, int c0, in
     bulk_commit_group();
   }
 }
-// The same to the output, or element by element where its rows are not whole 16-byte words.
+// The same to the output.  Rows that are not whole 16-byte words go element by
+// element, a row of the block at a time: neighbouring lanes write neighbouring
+// addresses, and each element is written (and added to) by one lane, the same
+// in every call.
 template <bool F32>
 __device__ __forceinline__ void wgrad_store(const WgradParams& P, int prob, int r0, int c0, int lane, uint8_t* buf,
                                             const float* v, bool adding) {
   constexpr int COLS = F32 ? 32 : 64;
   if (P.tma_out) {
     wgrad_tma_out<F32>(&P.map_o, c0, r0, prob, lane, buf, v, adding);
-  } else if (r0 + lane < P.M) {
-    const long long at = prob * P.out_bs + (long long)(r0 + lane) * P.N + c0;
+    return;
+  }
+  // (the buffer may still be read by a tensor store of a partial product)
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
 #pragma unroll
-    for (int j = 0; j < COLS; ++j) {
-      if (c0 + j < P.N) {
-        if constexpr (F32) {
-          float* o = static_cast<float*>(P.out) + at + j;
-          *o = adding ? *o + v[j] : v[j];
-        } else {
-          static_cast<__nv_bfloat16*>(P.out)[at + j] = __float2bfloat16_rn(v[j]);
-        }
+  for (int c = 0; c < 8; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = F32 ? __float_as_uint(v[4 * c + i]) : pack_bf16x2(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
+    *reinterpret_cast<uint4*>(buf + epi_swz(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  const long long base = prob * P.out_bs + c0;
+  const int n = min(32, P.M - r0);
+#pragma unroll 4
+  for (int r = 0; r < n; ++r) {
+    const long long at = base + (long long)(r0 + r) * P.N;
+#pragma unroll
+    for (int h = 0; h < COLS / 32; ++h) {
+      const int j = 32 * h + lane;
+      if (c0 + j >= P.N) continue;
+      if constexpr (F32) {
+        const float x = *reinterpret_cast<const float*>(buf + epi_swz(r, j >> 2) + (j & 3) * 4);
+        float* o = static_cast<float*>(P.out) + at + j;
+        *o = adding ? *o + x : x;
+      } else {
+        static_cast<uint16_t*>(P.out)[at + j] = *reinterpret_cast<const uint16_t*>(buf + epi_swz(r, j >> 3) + (j & 7) * 2);
       }
     }
   }
+  __syncwarp();
 }
 
 template <bool F32>
@@ -550,11 +572,19 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict
   }
 }
 
-// dY with rows that TMA cannot step over (not whole 16-byte words), to rows of `ld` elements.
-__global__ void __launch_bounds__(256) wgrad_copy_kernel(const __nv_bfloat16* __restrict__ src, __nv_bfloat16* __restrict__ dst,
-                                                         long long rows, int cols, int ld) {
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < cols; c += 256) dst[r * ld + c] = src[r * cols + c];
+// dY with rows that TMA cannot step over (not whole 16-byte words), to rows of
+// `ld` elements (even): two columns a thread, so that the stores are whole words.
+__global__ void __launch_bounds__(256) wgrad_copy_kernel(const uint16_t* __restrict__ src, uint32_t* __restrict__ dst, long long rows,
+                                                         int cols, int ld) {
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+    const uint16_t* s = src + r * cols;
+    uint32_t* d = dst + r * (ld / 2);
+#pragma unroll 4
+    for (int c = threadIdx.x; c < (cols + 1) / 2; c += 256) {
+      const uint32_t lo = s[2 * c], hi = 2 * c + 1 < cols ? s[2 * c + 1] : 0u;
+      d[c] = lo | (hi << 16);
+    }
+  }
 }
 
 }  // namespace mc

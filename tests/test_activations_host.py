@@ -35,6 +35,7 @@ def test_structure_size(lib):
     (dict(fmt=3), mc.MC_ERR_INVAL), (dict(cols=0), mc.MC_ERR_INVAL), (dict(rows=-1), mc.MC_ERR_INVAL),
     (dict(rows=1 << 31), mc.MC_ERR_INVAL), (dict(q_ld=72), mc.MC_ERR_INVAL), (dict(q_ld=48), mc.MC_ERR_INVAL),
     (dict(s_ld=8), mc.MC_ERR_INVAL), (dict(cols=1024, q_ld=1024, s_ld=16), mc.MC_ERR_INVAL), (dict(q=None), mc.MC_ERR_INVAL),
+    (dict(q_ld=1 << 31), mc.MC_ERR_INVAL), (dict(s_ld=1 << 31), mc.MC_ERR_INVAL),
     (dict(q=0x1000008), mc.MC_ERR_ALIGN), (dict(s=0x2000004), mc.MC_ERR_ALIGN)])
 def test_bad_act8_is_refused_everywhere(lib, bad, code):
     a = act8(**bad)

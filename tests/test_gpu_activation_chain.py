@@ -289,6 +289,29 @@ def test_workspaces_and_alignment():
     ok()
 
 
+def test_no_rows_at_all():
+    """Every operator on an empty batch."""
+    e, w, none = torch.empty(0, 64, dtype=BF, device=DEV), draw(1, 64), torch.empty(0, 2, device=DEV)
+    for fmt in (None, "e4m3"):
+        n = mc.rms_norm(e, w, residual=e.clone(), fmt=fmt)
+        assert n.h.shape == (0, 64) and n.rstd.shape == (0,) and tuple(n.y.shape) == (0, 64)
+    dx, dw = mc.rms_norm_backward(e, e.clone(), w, n.rstd)
+    assert dx.shape == (0, 64) and dw.shape == (64,) and (dw == 0).all()
+    plan = mc.expert_sort(torch.empty(0, 2, dtype=torch.int64, device=DEV), 3)
+    rows = mc.expert_gather(e, plan)
+    assert rows.shape == (0, 64) and mc.expert_combine(rows, plan, none).shape == (0, 64)
+    dy, dwt = mc.expert_combine_backward(e, rows, plan, none)
+    assert dy.shape == (0, 64) and dwt.shape == (0, 2)
+    x8 = mc.act8_pack(e)
+    for gather in (True, False):
+        g = mc.expert_weight_grad(e, x8, plan, gather=gather)
+        assert g.shape == (3, 64, 64) and (g == 0).all()
+    base = draw(2, 3, 64, 64, dtype=F32)
+    g = mc.expert_weight_grad(e, x8, plan, gather=True, out=base.clone(), accumulate=True)
+    assert torch.equal(g, base)
+    ok()
+
+
 def test_kernels_are_profiled():
     mc.profile_begin()
     Layer(90).run()

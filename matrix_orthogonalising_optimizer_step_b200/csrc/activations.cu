@@ -927,8 +927,17 @@ MC_API int mc_expert_combine_backward(const void* dout, const void* y, int dtype
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tokens, INT32_MAX));
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
+    const int runs = static_cast<int>((cols + run_cols<T>() - 1) / run_cols<T>());
+    int warps = 1, idle = INT_MAX;
+    for (int w = std::min(runs, MOVE_THREADS / 32); w >= 1 && w >= std::min(runs, 4); --w) {
+      const int left = (runs + w - 1) / w * w - runs;
+      if (left < idle) {
+        idle = left;
+        warps = w;
+      }
+    }
     with_bool(cols * es % 16 == 0, [&](auto v) {
-      expert_combine_bwd_kernel<T, decltype(v)::value><<<blocks, MOVE_THREADS, 0, s>>>(
+      expert_combine_bwd_kernel<T, decltype(v)::value><<<blocks, 32 * warps, 0, s>>>(
           static_cast<const T*>(dout), static_cast<const T*>(y), position, weights, static_cast<T*>(dy), dweights, tokens, top_k,
           static_cast<int>(cols));
     });

@@ -382,9 +382,10 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* _
   }
 }
 
-// One block per token: its 8 warps share the row, every pair's dot product is
-// kept by thread over the whole row and joined at the end (lanes by a tree,
-// then warps in order).  dy may be y itself: a thread reads what it overwrites.
+// One block per token: its warps (as many, up to 8, as leave the fewest idle in
+// the last of their turns over the row's 512-byte runs) share the row, every
+// pair's dot product is kept by thread over the whole row and joined at the end
+// (lanes by a tree, then warps in order).  dy may be y itself: a thread reads what it overwrites.
 // Four pairs' loads are in flight at a time; more would cost the registers
 // that let three blocks share an SM (all eight at once: one block, 260 us for
 // 4096 tokens of 8 pairs of 7168 bf16 columns; so: see the launch's figure).
@@ -397,8 +398,8 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(con
                                                                              float* __restrict__ dweights, long long tokens, int K,
                                                                              int D) {
   constexpr int N = move_elems<T>();
-  constexpr int WARPS = MOVE_THREADS / 32;
-  __shared__ float part[WARPS][BACK_PAIRS];
+  __shared__ float part[MOVE_THREADS / 32][BACK_PAIRS];
+  const int warps = blockDim.x >> 5;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long rows = tokens * K;
   for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(con
       float dot[BACK_PAIRS];
 #pragma unroll
       for (int a = 0; a < BACK_PAIRS; ++a) dot[a] = 0.f;
-      for (int c0 = warp * run_cols<T>(); c0 < D; c0 += WARPS * run_cols<T>()) {
+      for (int c0 = warp * run_cols<T>(); c0 < D; c0 += warps * run_cols<T>()) {
         float g[N];
         move_floats<T>(move_load<T, VEC>(dout + t * D, c0, lane, D), g);
 #pragma unroll
@@ -450,8 +451,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(con
       __syncthreads();
       if (threadIdx.x < BACK_PAIRS && k0 + static_cast<int>(threadIdx.x) < K) {
         float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += part[w][threadIdx.x];
+        for (int w = 0; w < warps; ++w) s += part[w][threadIdx.x];
         dweights[t * K + k0 + threadIdx.x] = s;  // 0 for a dropped pair
       }
       __syncthreads();

@@ -218,21 +218,36 @@ __device__ __forceinline__ void wgrad_store(const WgradParams& P, int prob, int 
     *reinterpret_cast<uint4*>(buf + epi_swz(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
-  const long long base = prob * P.out_bs + c0;
-  const int n = min(32, P.M - r0);
-#pragma unroll 4
-  for (int r = 0; r < n; ++r) {
-    const long long at = base + (long long)(r0 + r) * P.N;
+  const long long base = prob * P.out_bs + (long long)r0 * P.N + c0;
+  const int rows = min(32, P.M - r0), cols = min(COLS, P.N - c0);
+  constexpr int AHEAD = 4;  // rows read from the buffer before the first is stored (8 and 16: slower)
+#pragma unroll 1
+  for (int rb = 0; rb < rows; rb += AHEAD) {
 #pragma unroll
     for (int h = 0; h < COLS / 32; ++h) {
       const int j = 32 * h + lane;
-      if (c0 + j >= P.N) continue;
       if constexpr (F32) {
-        const float x = *reinterpret_cast<const float*>(buf + epi_swz(r, j >> 2) + (j & 3) * 4);
-        float* o = static_cast<float*>(P.out) + at + j;
-        *o = adding ? *o + x : x;
+        float* o = static_cast<float*>(P.out) + base + (long long)rb * P.N + j;
+        float x[AHEAD], old[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) x[i] = *reinterpret_cast<const float*>(buf + epi_swz(rb + i, j >> 2) + (j & 3) * 4);
+        if (adding) {
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) old[i] = (rb + i < rows && j < cols) ? o[(long long)i * P.N] : 0.f;
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) x[i] += old[i];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (rb + i < rows && j < cols) o[(long long)i * P.N] = x[i];
       } else {
-        static_cast<uint16_t*>(P.out)[at + j] = *reinterpret_cast<const uint16_t*>(buf + epi_swz(r, j >> 3) + (j & 7) * 2);
+        uint16_t* o = static_cast<uint16_t*>(P.out) + base + (long long)rb * P.N + j;
+        uint16_t x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) x[i] = *reinterpret_cast<const uint16_t*>(buf + epi_swz(rb + i, j >> 3) + (j & 7) * 2);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (rb + i < rows && j < cols) o[(long long)i * P.N] = x[i];
       }
     }
   }

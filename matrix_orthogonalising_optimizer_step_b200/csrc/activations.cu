@@ -192,6 +192,13 @@ void with_bool(bool b, F&& f) {
   if (b) f(std::true_type{});
   else f(std::false_type{});
 }
+// Bytes of an access that every row of `cols` elements begins on a boundary of.
+template <typename T, typename F>
+void with_width(int64_t cols, F&& f) {
+  if (cols * int64_t(sizeof(T)) % 16 == 0) f(std::integral_constant<int, 16>{});
+  else if (sizeof(T) == 4 || cols % 2 == 0) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, int(sizeof(T))>{});
+}
 template <typename F>
 void with_fmt(int fmt, F&& f) {
   if (fmt == MC_ACT_E4M3) f(std::integral_constant<int, ACT_E4M3>{});
@@ -866,7 +873,7 @@ MC_API int mc_expert_gather(const void* x, int dtype, int64_t tokens, int top_k,
     const int seg_cols = GATHER_RUNS * run_cols<T>();
     const int segments = static_cast<int>((cols + seg_cols - 1) / seg_cols);
     const unsigned blocks = item_blocks(tokens * segments, 1, MOVE_THREADS / 32, st->sms);
-    with_bool(cols * es % 16 == 0, [&](auto v) {
+    with_width<T>(cols, [&](auto v) {
       expert_gather_kernel<T, decltype(v)::value><<<blocks, MOVE_THREADS, 0, s>>>(static_cast<const T*>(x), position, static_cast<T*>(rows_out),
                                                                                  tokens, top_k, static_cast<int>(cols), segments);
     });
@@ -896,7 +903,7 @@ MC_API int mc_expert_combine(const void* y, int dtype, int64_t tokens, int top_k
     const int seg_cols = COMBINE_RUNS * run_cols<T>();
     const int segments = static_cast<int>((cols + seg_cols - 1) / seg_cols);
     const unsigned blocks = item_blocks(tokens * segments, 1, MOVE_THREADS / 32, st->sms);
-    with_bool(cols * es % 16 == 0, [&](auto v) {
+    with_width<T>(cols, [&](auto v) {
       expert_combine_kernel<T, decltype(v)::value><<<blocks, MOVE_THREADS, 0, s>>>(
           static_cast<const T*>(y), position, weights, static_cast<T*>(out), tokens, top_k, static_cast<int>(cols), segments);
     });
@@ -936,7 +943,7 @@ MC_API int mc_expert_combine_backward(const void* dout, const void* y, int dtype
         warps = w;
       }
     }
-    with_bool(cols * es % 16 == 0, [&](auto v) {
+    with_width<T>(cols, [&](auto v) {
       expert_combine_bwd_kernel<T, decltype(v)::value><<<blocks, 32 * warps, 0, s>>>(
           static_cast<const T*>(dout), static_cast<const T*>(y), position, weights, static_cast<T*>(dy), dweights, tokens, top_k,
           static_cast<int>(cols));

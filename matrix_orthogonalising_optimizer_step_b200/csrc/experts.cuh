@@ -224,47 +224,47 @@ __global__ void __launch_bounds__(THREADS) expert_place_kernel(const I* __restri
 // Items are (token, segment of columns), one per warp and step.
 constexpr int MOVE_THREADS = 256;
 
-// One lane's share of a segment: 16 bytes of each of MOVE_VECS 512-byte runs
-// (VEC), or single elements of them.
+// One lane's share of a run of 512 bytes: 16 of them at once (W = 16: rows of
+// whole 16-byte words), or 4-byte words (W = 4: rows of whole words) or single
+// bf16 elements (W = 2) that neighbouring lanes have neighbours of.
 template <typename T>
 __host__ __device__ constexpr int move_elems() { return 16 / int(sizeof(T)); }
 
-template <typename T, bool VEC>
+template <typename T, int W>
 __device__ __forceinline__ uint4 move_load(const T* row, int c0, int lane, int D) {
-  constexpr int N = move_elems<T>();
-  if constexpr (VEC) {
-    const int c = c0 + N * lane;
+  constexpr int PER = W / int(sizeof(T));  // elements of an access
+  static_assert(W == 16 || W == 4 || (W == 2 && sizeof(T) == 2), "whole elements");
+  if constexpr (W == 16) {
+    const int c = c0 + PER * lane;
     return c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
   } else {
-    union {
-      uint4 q;
-      T e[N];
-    } u;
-    u.q = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = c0 + 32 * i + lane;
-      if (c < D) u.e[i] = row[c];
+    for (int i = 0; i < 16 / W; ++i) {
+      const int c = c0 + PER * (32 * i + lane);
+      if (c < D) {
+        if constexpr (W == 4) w[i] = *reinterpret_cast<const uint32_t*>(row + c);
+        else w[i >> 1] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(row + c)) << (16 * (i & 1));
+      }
     }
-    return u.q;
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-template <typename T, bool VEC>
+template <typename T, int W>
 __device__ __forceinline__ void move_store(T* row, int c0, int lane, int D, uint4 q) {
-  constexpr int N = move_elems<T>();
-  if constexpr (VEC) {
-    const int c = c0 + N * lane;
+  constexpr int PER = W / int(sizeof(T));
+  if constexpr (W == 16) {
+    const int c = c0 + PER * lane;
     if (c < D) *reinterpret_cast<uint4*>(row + c) = q;
   } else {
-    union {
-      uint4 q;
-      T e[N];
-    } u;
-    u.q = q;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = c0 + 32 * i + lane;
-      if (c < D) row[c] = u.e[i];
+    for (int i = 0; i < 16 / W; ++i) {
+      const int c = c0 + PER * (32 * i + lane);
+      if (c < D) {
+        if constexpr (W == 4) *reinterpret_cast<uint32_t*>(row + c) = w[i];
+        else *reinterpret_cast<uint16_t*>(row + c) = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+      }
     }
   }
 }
@@ -294,7 +294,7 @@ template <typename T>
 __host__ __device__ constexpr int run_cols() { return 32 * move_elems<T>(); }  // columns of one 512-byte run
 
 constexpr int GATHER_RUNS = 4;
-template <typename T, bool VEC>
+template <typename T, int W>
 __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const T* __restrict__ x, const int* __restrict__ position,
                                                                      T* __restrict__ out, long long tokens, int K, int D,
                                                                      int segments) {
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const T* __
     const int c0 = w.chunk * GATHER_RUNS * run_cols<T>();
     uint4 q[GATHER_RUNS];
 #pragma unroll
-    for (int u = 0; u < GATHER_RUNS; ++u) q[u] = move_load<T, VEC>(x + w.row * D, c0 + u * run_cols<T>(), lane, D);
+    for (int u = 0; u < GATHER_RUNS; ++u) q[u] = move_load<T, W>(x + w.row * D, c0 + u * run_cols<T>(), lane, D);
     for (int k0 = 0; k0 < K; k0 += 32) {
       const int mine = k0 + lane < K ? position[w.row * K + k0 + lane] : -1;
       const int kn = min(32, K - k0);
@@ -318,14 +318,14 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const T* __
         if (r < 0 || r >= rows) continue;
 #pragma unroll
         for (int u = 0; u < GATHER_RUNS; ++u)
-          move_store<T, VEC>(out + (long long)r * D, c0 + u * run_cols<T>(), lane, D, q[u]);
+          move_store<T, W>(out + (long long)r * D, c0 + u * run_cols<T>(), lane, D, q[u]);
       }
     }
   }
 }
 
 constexpr int COMBINE_RUNS = 2;
-template <typename T, bool VEC>
+template <typename T, int W>
 __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* __restrict__ y, const int* __restrict__ position,
                                                                       const float* __restrict__ weights, T* __restrict__ out,
                                                                       long long tokens, int K, int D, int segments) {
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* _
           if (live[a]) {
 #pragma unroll
             for (int u = 0; u < COMBINE_RUNS; ++u)
-              q[a][u] = move_load<T, VEC>(y + (long long)r * D, c0 + u * run_cols<T>(), lane, D);
+              q[a][u] = move_load<T, W>(y + (long long)r * D, c0 + u * run_cols<T>(), lane, D);
           }
         }
 #pragma unroll
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* _
     }
 #pragma unroll
     for (int u = 0; u < COMBINE_RUNS; ++u)
-      move_store<T, VEC>(out + w.row * D, c0 + u * run_cols<T>(), lane, D, move_words<T>(sum[u]));
+      move_store<T, W>(out + w.row * D, c0 + u * run_cols<T>(), lane, D, move_words<T>(sum[u]));
   }
 }
 
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* _
 // 4096 tokens of 8 pairs of 7168 bf16 columns; so: see the launch's figure).
 constexpr int BACK_PAIRS = 8;  // pairs whose sums a pass over the row keeps
 constexpr int BACK_AHEAD = 4;  // pairs loaded together
-template <typename T, bool VEC>
+template <typename T, int W>
 __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(const T* __restrict__ dout, const T* y,
                                                                              const int* __restrict__ position,
                                                                              const float* __restrict__ weights, T* dy,
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(con
       for (int a = 0; a < BACK_PAIRS; ++a) dot[a] = 0.f;
       for (int c0 = warp * run_cols<T>(); c0 < D; c0 += warps * run_cols<T>()) {
         float g[N];
-        move_floats<T>(move_load<T, VEC>(dout + t * D, c0, lane, D), g);
+        move_floats<T>(move_load<T, W>(dout + t * D, c0, lane, D), g);
 #pragma unroll
         for (int a0 = 0; a0 < BACK_PAIRS; a0 += BACK_AHEAD) {
           uint4 q[BACK_AHEAD];
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(con
 #pragma unroll
           for (int a = 0; a < BACK_AHEAD; ++a) {
             pos[a] = __shfl_sync(0xffffffffu, mine, a0 + a);
-            if (pos[a] >= 0) q[a] = move_load<T, VEC>(y + (long long)pos[a] * D, c0, lane, D);
+            if (pos[a] >= 0) q[a] = move_load<T, W>(y + (long long)pos[a] * D, c0, lane, D);
           }
 #pragma unroll
           for (int a = 0; a < BACK_AHEAD; ++a) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_bwd_kernel(con
               dot[a0 + a] = fmaf(g[i], v[i], dot[a0 + a]);
               v[i] = wk * g[i];
             }
-            move_store<T, VEC>(dy + (long long)pos[a] * D, c0, lane, D, move_words<T>(v));
+            move_store<T, W>(dy + (long long)pos[a] * D, c0, lane, D, move_words<T>(v));
           }
         }
       }

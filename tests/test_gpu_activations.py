@@ -359,7 +359,7 @@ def test_sort_of_unlike_loads():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("T,K,E,D", [(1, 1, 2, 8), (1, 8, 64, 7168), (48, 8, 64, 1000), (130, 2, 4, 33), (33, 6, 16, 1), (9, 40, 50, 264), (500, 4, 8, 513)])
+@pytest.mark.parametrize("T,K,E,D", [(1, 1, 2, 8), (1, 8, 64, 7168), (48, 8, 64, 1000), (130, 2, 4, 33), (33, 6, 16, 1), (9, 40, 50, 264), (500, 4, 8, 513), (60, 3, 8, 1598), (7, 2, 4, 30)])
 def test_gather_combine_and_gradient(T, K, E, D, dtype):
     idx, weights = routing(T + D, T, K, E)
     plan = check_sort(idx, E)

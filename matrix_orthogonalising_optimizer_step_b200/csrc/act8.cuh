@@ -13,11 +13,15 @@
 // bf16 numbers gets the same bytes.
 //
 // All kernels here and the norm kernels share one mapping of columns to
-// threads: a warp holds 256 consecutive columns of a row, eight values a
-// lane.  VEC (rows of whole 16-byte words): lane l holds columns 8l..8l+7, a
-// block is four neighbouring lanes.  Otherwise: value i of lane l is column
-// 32i + l, a block is one value of all 32 lanes; single elements are loaded,
-// but neighbouring lanes still touch neighbouring addresses.
+// threads: a warp holds 256 consecutive columns of a row, eight values a lane,
+// in groups of G neighbours that one access moves:
+//   G = 8  rows of whole 16-byte words: lane l holds columns 8l..8l+7, a block is
+//          four neighbouring lanes
+//   G = 2  even widths: value 2p, 2p + 1 of lane l are columns 64p + 2l, + 1, a
+//          block is one pair of half a warp
+//   G = 1  odd widths: value i of lane l is column 32i + l, a block is one value
+//          of all lanes
+// Neighbouring lanes always touch neighbouring addresses.
 #pragma once
 
 #include "ptx.cuh"
@@ -29,129 +33,108 @@ constexpr int ACT_BLOCK = 32;
 constexpr int WARP_COLS = 256;
 
 // ---------------------------------------------------------------- fragments
-template <bool VEC>
-__device__ __forceinline__ int frag_col(int c0, int lane, int i) {
-  return VEC ? c0 + 8 * lane + i : c0 + 32 * i + lane;
-}
+template <int G>
+__device__ __forceinline__ int frag_col(int c0, int lane, int i) { return c0 + (i / G) * 32 * G + lane * G + i % G; }
 
 // Raw words of one fragment: loaded early, turned into floats when needed.
 template <typename T>
-struct RawFrag;
-template <>
-struct RawFrag<__nv_bfloat16> {
-  uint4 q;
-};
-template <>
-struct RawFrag<float> {
-  float4 a, b;
+struct RawFrag {
+  uint32_t w[2 * sizeof(T)];
 };
 
-template <bool VEC>
-__device__ __forceinline__ void load_frag(RawFrag<__nv_bfloat16>& f, const __nv_bfloat16* row, int c0, int lane, int D) {
-  if constexpr (VEC) {
-    const int c = c0 + 8 * lane;
-    f.q = c < D ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    uint32_t w[4];
+// The fragment's columns of a row of D; those at or past D as zeros.  Rows begin
+// on a boundary of G elements (16 bytes at most).
+template <int G, typename T>
+__device__ __forceinline__ void load_frag(RawFrag<T>& f, const T* row, int c0, int lane, int D) {
+  constexpr int BYTES = G * int(sizeof(T));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ca = c0 + 64 * i + lane, cb = ca + 32;
-      const uint32_t lo = ca < D ? *reinterpret_cast<const uint16_t*>(row + ca) : 0u;
-      const uint32_t hi = cb < D ? *reinterpret_cast<const uint16_t*>(row + cb) : 0u;
-      w[i] = lo | (hi << 16);
+  for (int i = 0; i < 8; i += G) {
+    const int c = frag_col<G>(c0, lane, i);
+    const bool in = c < D;
+    uint32_t* w = f.w + i * int(sizeof(T)) / 4;
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int k = 0; k < BYTES / 16; ++k) {
+        const uint4 q = in ? reinterpret_cast<const uint4*>(row + c)[k] : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * k] = q.x;
+        w[4 * k + 1] = q.y;
+        w[4 * k + 2] = q.z;
+        w[4 * k + 3] = q.w;
+      }
+    } else if constexpr (BYTES == 8) {
+      const uint2 q = in ? *reinterpret_cast<const uint2*>(row + c) : make_uint2(0u, 0u);
+      w[0] = q.x;
+      w[1] = q.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = in ? *reinterpret_cast<const uint32_t*>(row + c) : 0u;
+    } else {
+      const uint32_t h = in ? *reinterpret_cast<const uint16_t*>(row + c) : 0u;
+      w[0] = (i & 1) ? w[0] | (h << 16) : h;
     }
-    f.q = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load_frag(RawFrag<float>& f, const float* row, int c0, int lane, int D) {
-  if constexpr (VEC) {
-    const int c = c0 + 8 * lane;
-    const float4* p = reinterpret_cast<const float4*>(row + c);
-    f.a = c < D ? p[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-    f.b = c < D ? p[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-  } else {
-    float w[8];
+// The fragment as it is to memory, none of it at or past D.
+template <int G, typename T>
+__device__ __forceinline__ void store_raw(T* row, int c0, int lane, int D, const RawFrag<T>& f) {
+  constexpr int BYTES = G * int(sizeof(T));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + 32 * i + lane;
-      w[i] = c < D ? row[c] : 0.f;
+  for (int i = 0; i < 8; i += G) {
+    const int c = frag_col<G>(c0, lane, i);
+    if (c >= D) continue;
+    const uint32_t* w = f.w + i * int(sizeof(T)) / 4;
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int k = 0; k < BYTES / 16; ++k)
+        reinterpret_cast<uint4*>(row + c)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    } else if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+    } else if constexpr (BYTES == 4) {
+      *reinterpret_cast<uint32_t*>(row + c) = w[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(row + c) = static_cast<uint16_t>((i & 1) ? w[0] >> 16 : w[0]);
     }
-    f.a = make_float4(w[0], w[1], w[2], w[3]);
-    f.b = make_float4(w[4], w[5], w[6], w[7]);
   }
 }
+
 __device__ __forceinline__ void frag_floats(const RawFrag<__nv_bfloat16>& f, float (&v)[8]) {
-  const uint32_t w[4] = {f.q.x, f.q.y, f.q.z, f.q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    v[2 * i] = __uint_as_float(f.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(f.w[i] & 0xFFFF0000u);
   }
 }
 __device__ __forceinline__ void frag_floats(const RawFrag<float>& f, float (&v)[8]) {
-  v[0] = f.a.x; v[1] = f.a.y; v[2] = f.a.z; v[3] = f.a.w;
-  v[4] = f.b.x; v[5] = f.b.y; v[6] = f.b.z; v[7] = f.b.w;
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store_frag(__nv_bfloat16* row, int c0, int lane, int D, const float (&v)[8]) {
-  if constexpr (VEC) {
-    const int c = c0 + 8 * lane;
-    if (c < D)
-      *reinterpret_cast<uint4*>(row + c) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + 32 * i + lane;
-      if (c < D) row[c] = __float2bfloat16_rn(v[i]);
-    }
-  }
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(f.w[i]);
 }
-template <bool VEC>
-__device__ __forceinline__ void store_frag(float* row, int c0, int lane, int D, const float (&v)[8]) {
-  if constexpr (VEC) {
-    const int c = c0 + 8 * lane;
-    if (c < D) {
-      float4* p = reinterpret_cast<float4*>(row + c);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
+// Values rounded to the fragment's type.
+__device__ __forceinline__ void frag_round(RawFrag<__nv_bfloat16>& f, const float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + 32 * i + lane;
-      if (c < D) row[c] = v[i];
-    }
-  }
+  for (int i = 0; i < 4; ++i) f.w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
 }
-
+__device__ __forceinline__ void frag_round(RawFrag<float>& f, const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.w[i] = __float_as_uint(v[i]);
+}
 // f + g, rounded to the type.  Two bf16 numbers: their sum is exact in fp32
 // unless they are so far apart (over 2^16) that it rounds to the larger one, so
 // one rounding and the detour over fp32 give the same.
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&s);
-}
 __device__ __forceinline__ void frag_add(RawFrag<__nv_bfloat16>& f, const RawFrag<__nv_bfloat16>& g) {
-  f.q = make_uint4(add_bf16x2(f.q.x, g.q.x), add_bf16x2(f.q.y, g.q.y), add_bf16x2(f.q.z, g.q.z), add_bf16x2(f.q.w, g.q.w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&f.w[i]), *reinterpret_cast<const __nv_bfloat162*>(&g.w[i]));
+    f.w[i] = *reinterpret_cast<const uint32_t*>(&s);
+  }
 }
 __device__ __forceinline__ void frag_add(RawFrag<float>& f, const RawFrag<float>& g) {
-  f.a = make_float4(f.a.x + g.a.x, f.a.y + g.a.y, f.a.z + g.a.z, f.a.w + g.a.w);
-  f.b = make_float4(f.b.x + g.b.x, f.b.y + g.b.y, f.b.z + g.b.z, f.b.w + g.b.w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.w[i] = __float_as_uint(__uint_as_float(f.w[i]) + __uint_as_float(g.w[i]));
 }
-// The fragment as it is to memory.
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_raw(T* row, int c0, int lane, int D, const RawFrag<T>& f) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    const int c = c0 + 8 * lane;
-    if (c < D) *reinterpret_cast<uint4*>(row + c) = f.q;
-  } else {
-    float v[8];
-    frag_floats(f, v);
-    store_frag<VEC>(row, c0, lane, D, v);
-  }
+template <int G, typename T>
+__device__ __forceinline__ void store_frag(T* row, int c0, int lane, int D, const float (&v)[8]) {
+  RawFrag<T> f;
+  frag_round(f, v);
+  store_raw<G>(row, c0, lane, D, f);
 }
 
 // max(|a|, |b|), NaN if either is
@@ -201,9 +184,9 @@ __device__ __forceinline__ float2 act_decode2(uint32_t two) {
 }
 
 // One fragment to 8 bits.  All 32 lanes take part; columns at or past D hold 0.
-template <int FMT, bool VEC>
+template <int FMT, int G>
 __device__ __forceinline__ void store_frag8(uint8_t* qrow, uint8_t* srow, int c0, int lane, int D, const float (&v)[8]) {
-  if constexpr (VEC) {
+  if constexpr (G == 8) {
     float big = max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])), max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])));
     big = max_abs(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = max_abs(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -221,24 +204,36 @@ __device__ __forceinline__ void store_frag8(uint8_t* qrow, uint8_t* srow, int c0
       if ((lane & 3) == 0) srow[c / ACT_BLOCK] = fine ? static_cast<uint8_t>(k + 127) : 255;
     }
   } else {
-    // lane i (mod 8) works out block i's scale, for all lanes
+    // `PER` blocks share the lanes at a time (halves of the warp, or all of it);
+    // the lane that is to a block what `duty` is to it works its scale out for all
+    constexpr int PER = G, TURNS = 8 / G;
+    const int part = PER == 2 ? lane >> 4 : 0, duty = lane & (TURNS - 1);
+    const unsigned mask = PER == 2 ? 0x0000FFFFu << (16 * part) : 0xFFFFFFFFu;
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t mi = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      if ((lane & 7) == i) m = mi;
+    for (int t = 0; t < TURNS; ++t) {
+      const float big = PER == 2 ? max_abs(v[2 * t], v[2 * t + 1]) : fabsf(v[t]);
+      const uint32_t mt = __reduce_max_sync(mask, __float_as_uint(big));
+      if (duty == t) m = mt;
     }
     const bool fine = m < 0x7F800000u;
     const int k = act_exponent<FMT>(m);
     const float r = fine ? exp2_int(-k) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float ri = __shfl_sync(0xffffffffu, r, i);
-      const uint32_t code = act_encode2<FMT>(v[i] * ri, 0.f);
-      const int c = c0 + 32 * i + lane;
-      if (c < D) qrow[c] = ri > 0.f ? static_cast<uint8_t>(code) : 0;
+    for (int t = 0; t < TURNS; ++t) {
+      const float rt = __shfl_sync(0xffffffffu, r, 16 * part + t);
+      const int c = frag_col<G>(c0, lane, t * G);
+      if constexpr (PER == 2) {
+        const uint32_t two = act_encode2<FMT>(v[2 * t] * rt, v[2 * t + 1] * rt);
+        if (c < D) *reinterpret_cast<uint16_t*>(qrow + c) = rt > 0.f ? static_cast<uint16_t>(two) : 0;
+      } else {
+        const uint32_t one = act_encode2<FMT>(v[t] * rt, 0.f);
+        if (c < D) qrow[c] = rt > 0.f ? static_cast<uint8_t>(one) : 0;
+      }
     }
-    if (lane < 8 && c0 + 32 * lane < D) srow[c0 / ACT_BLOCK + lane] = fine ? static_cast<uint8_t>(k + 127) : 255;
+    const int b = PER * duty + part;  // this lane's block of the 256 columns
+    if ((lane & (PER == 2 ? 15 : 31)) < TURNS && c0 + ACT_BLOCK * b < D)
+      srow[c0 / ACT_BLOCK + b] = fine ? static_cast<uint8_t>(k + 127) : 255;
   }
 }
 
@@ -247,26 +242,27 @@ struct Raw8 {
   uint2 q;
   uint2 s;
 };
-template <bool VEC>
+template <int G>
 __device__ __forceinline__ void load_frag8(Raw8& f, const uint8_t* qrow, const uint8_t* srow, int c0, int lane, int D) {
-  if constexpr (VEC) {
+  if constexpr (G == 8) {
     const int c = c0 + 8 * lane;
     f.q = c < D ? *reinterpret_cast<const uint2*>(qrow + c) : make_uint2(0u, 0u);
     f.s.x = c < D ? srow[c / ACT_BLOCK] : 0u;
   } else {
     // the eight scale bytes of these columns (srow rows are 16-byte aligned and padded to 16 bytes)
-    f.s = *reinterpret_cast<const uint2*>(srow + c0 / ACT_BLOCK);
+    f.s = c0 < D ? *reinterpret_cast<const uint2*>(srow + c0 / ACT_BLOCK) : make_uint2(0u, 0u);
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + 32 * i + lane;
-      const uint32_t b = c < D ? qrow[c] : 0u;
+    for (int i = 0; i < 8; i += G) {
+      const int c = frag_col<G>(c0, lane, i);
+      uint32_t b = 0u;
+      if (c < D) b = G == 2 ? *reinterpret_cast<const uint16_t*>(qrow + c) : qrow[c];
       w[i >> 2] |= b << (8 * (i & 3));
     }
     f.q = make_uint2(w[0], w[1]);
   }
 }
-template <int FMT, bool VEC>
+template <int FMT, int G>
 __device__ __forceinline__ void frag8_floats(const Raw8& f, int c0, int lane, int D, float (&v)[8]) {
   const uint32_t w[2] = {f.q.x, f.q.y};
 #pragma unroll
@@ -277,16 +273,19 @@ __device__ __forceinline__ void frag8_floats(const Raw8& f, int c0, int lane, in
     v[4 * i + 2] = b.x;
     v[4 * i + 3] = b.y;
   }
-  if constexpr (VEC) {
+  if constexpr (G == 8) {
     const float s = act_scale_value(f.s.x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= s;
   } else {
     // a column past D multiplies by no scale: the bytes behind the last block are not read as one
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t s = ((i < 4 ? f.s.x : f.s.y) >> (8 * (i & 3))) & 0xFFu;
-      v[i] = c0 + 32 * i + lane < D ? v[i] * act_scale_value(s) : 0.f;
+    for (int i = 0; i < 8; i += G) {
+      const int b = G == 2 ? i + (lane >> 4) : i;  // block of the 256 columns
+      const uint32_t s = ((b < 4 ? f.s.x : f.s.y) >> (8 * (b & 3))) & 0xFFu;
+      const float x = act_scale_value(s);
+#pragma unroll
+      for (int j = i; j < i + G; ++j) v[j] = frag_col<G>(c0, lane, j) < D ? v[j] * x : 0.f;
     }
   }
 }
@@ -309,7 +308,7 @@ __device__ __forceinline__ void walk_next(RowWalk& w, long long step_rows, int s
 
 constexpr int ACT_THREADS = 256;
 
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int G>
 __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                                 uint8_t* __restrict__ s, long long rows, int D,
                                                                 long long q_ld, long long s_ld, int chunks) {
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restr
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       at[u] = w;
-      if (w.row < rows) load_frag<VEC>(f[u], x + w.row * D, w.chunk * WARP_COLS, lane, D);
+      if (w.row < rows) load_frag<G>(f[u], x + w.row * D, w.chunk * WARP_COLS, lane, D);
       walk_next(w, step_rows, step_chunks, chunks);
     }
 #pragma unroll
@@ -334,13 +333,13 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restr
       if (at[u].row >= rows) break;
       float v[8];
       frag_floats(f[u], v);
-      store_frag8<FMT, VEC>(q + at[u].row * q_ld, s + at[u].row * s_ld, at[u].chunk * WARP_COLS, lane, D, v);
+      store_frag8<FMT, G>(q + at[u].row * q_ld, s + at[u].row * s_ld, at[u].chunk * WARP_COLS, lane, D, v);
     }
   }
 }
 
 // The rows of an 8-bit activation to bf16 or fp32.
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int G>
 __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t* __restrict__ q,
                                                                   const uint8_t* __restrict__ s, T* __restrict__ out,
                                                                   long long rows, int D, long long q_ld,
@@ -359,15 +358,15 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       at[u] = w;
-      if (w.row < rows) load_frag8<VEC>(f[u], q + w.row * q_ld, s + w.row * s_ld, w.chunk * WARP_COLS, lane, D);
+      if (w.row < rows) load_frag8<G>(f[u], q + w.row * q_ld, s + w.row * s_ld, w.chunk * WARP_COLS, lane, D);
       walk_next(w, step_rows, step_chunks, chunks);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       if (at[u].row >= rows) break;
       float v[8];
-      frag8_floats<FMT, VEC>(f[u], at[u].chunk * WARP_COLS, lane, D, v);
-      store_frag<VEC>(out + at[u].row * out_ld, at[u].chunk * WARP_COLS, lane, D, v);
+      frag8_floats<FMT, G>(f[u], at[u].chunk * WARP_COLS, lane, D, v);
+      store_frag<G>(out + at[u].row * out_ld, at[u].chunk * WARP_COLS, lane, D, v);
     }
   }
 }
@@ -396,12 +395,12 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_scatter_kernel(const uint8_t
     Raw8 f[RUNS];
 #pragma unroll
     for (int u = 0; u < RUNS; ++u)
-      load_frag8<true>(f[u], q + w.row * q_ld, s + w.row * s_ld, c0 + u * WARP_COLS, lane, D);
+      load_frag8<8>(f[u], q + w.row * q_ld, s + w.row * s_ld, c0 + u * WARP_COLS, lane, D);
     uint4 v[RUNS];
 #pragma unroll
     for (int u = 0; u < RUNS; ++u) {
       float x[8];
-      frag8_floats<FMT, true>(f[u], c0 + u * WARP_COLS, lane, D, x);
+      frag8_floats<FMT, 8>(f[u], c0 + u * WARP_COLS, lane, D, x);
       v[u] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
     for (int k0 = 0; k0 < top_k; k0 += 32) {

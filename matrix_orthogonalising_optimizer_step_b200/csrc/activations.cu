@@ -63,6 +63,39 @@ int take_workspace(DeviceState* st, size_t need, void** ws, size_t bytes) {
   return own_workspace(*st, need, ws);
 }
 
+// ----------------------------------------------- run-time choices to constants
+template <typename F>
+void with_nv(int nv, F&& f) {
+  if (nv == 1) f(std::integral_constant<int, 1>{});
+  else if (nv == 2) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 4>{});
+}
+// Columns that one access moves: 8, 2 or 1, as the rows of `cols` columns begin.
+template <typename F>
+void with_group(int64_t cols, F&& f) {
+  if (cols % 8 == 0) f(std::integral_constant<int, 8>{});
+  else if (cols % 2 == 0) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 1>{});
+}
+// Bytes of an access that every row of `cols` elements begins on a boundary of.
+template <typename T, typename F>
+void with_width(int64_t cols, F&& f) {
+  if (cols * int64_t(sizeof(T)) % 16 == 0) f(std::integral_constant<int, 16>{});
+  else if (sizeof(T) == 4 || cols % 2 == 0) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, int(sizeof(T))>{});
+}
+template <typename F>
+void with_fmt(int fmt, F&& f) {
+  if (fmt == MC_ACT_E4M3) f(std::integral_constant<int, ACT_E4M3>{});
+  else if (fmt == MC_ACT_INT8) f(std::integral_constant<int, ACT_INT8>{});
+  else f(std::integral_constant<int, ACT_NONE>{});
+}
+template <typename F>
+void with_dtype(int dtype, F&& f) {
+  if (dtype == MC_F32) f(float{});
+  else f(__nv_bfloat16{});
+}
+
 // ------------------------------------------------------------ pack, unpack
 // Blocks for `items` warp items, `per` of them per warp and step: at most 32 a
 // SM, and every block as many steps.  More blocks than an SM holds at once (4 or
@@ -75,41 +108,37 @@ unsigned item_blocks(long long items, int per, int warps, int sms) {
   return static_cast<unsigned>(std::max<long long>(1, (want + steps - 1) / steps));
 }
 
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int G>
 void pack_launch(const void* x, const mc_act8* a, int chunks, unsigned blocks, cudaStream_t s) {
-  act8_pack_kernel<T, FMT, VEC><<<blocks, ACT_THREADS, 0, s>>>(
+  act8_pack_kernel<T, FMT, G><<<blocks, ACT_THREADS, 0, s>>>(
       static_cast<const T*>(x), static_cast<uint8_t*>(a->q), static_cast<uint8_t*>(a->scale), a->rows,
       static_cast<int>(a->cols), a->q_ld, a->s_ld, chunks);
 }
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int G>
 void unpack_launch(const mc_act8* a, void* out, int64_t rows, int64_t out_ld, int chunks,
                    unsigned blocks, cudaStream_t s) {
-  act8_unpack_kernel<T, FMT, VEC><<<blocks, ACT_THREADS, 0, s>>>(
+  act8_unpack_kernel<T, FMT, G><<<blocks, ACT_THREADS, 0, s>>>(
       static_cast<const uint8_t*>(a->q), static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), rows,
       static_cast<int>(a->cols), a->q_ld, a->s_ld, out_ld, chunks);
 }
 
 // The rows of `a` to `out`, rows of out_ld elements.
-int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, int64_t out_ld, bool vec, int kind, cudaStream_t s) {
+int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, int64_t out_ld, int kind, cudaStream_t s) {
   const int64_t rows = a->rows;
   if (rows == 0) return MC_OK;
   const int chunks = static_cast<int>((a->cols + WARP_COLS - 1) / WARP_COLS);
   const unsigned blocks = item_blocks(rows * chunks, 4, ACT_THREADS / 32, st.sms);
   const bool e4 = a->fmt == MC_ACT_E4M3;
   ProfScope prof(kind, s, 0, 0, double(rows) * a->cols * (dtype_bytes(dtype) + 1 + 1.0 / ACT_BLOCK));
-  auto go = [&](auto t, auto v) {
+  with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    constexpr bool V = decltype(v)::value;
-    if (e4) unpack_launch<T, ACT_E4M3, V>(a, out, rows, out_ld, chunks, blocks, s);
-    else unpack_launch<T, ACT_INT8, V>(a, out, rows, out_ld, chunks, blocks, s);
-  };
-  if (dtype == MC_F32) {
-    if (vec) go(float{}, std::true_type{});
-    else go(float{}, std::false_type{});
-  } else {
-    if (vec) go(__nv_bfloat16{}, std::true_type{});
-    else go(__nv_bfloat16{}, std::false_type{});
-  }
+    // rows of `out` may be padded to whole words, which are then written whole
+    with_group(out_ld % 8 == 0 ? 8 : a->cols, [&](auto g) {
+      constexpr int G = decltype(g)::value;
+      if (e4) unpack_launch<T, ACT_E4M3, G>(a, out, rows, out_ld, chunks, blocks, s);
+      else unpack_launch<T, ACT_INT8, G>(a, out, rows, out_ld, chunks, blocks, s);
+    });
+  });
   MC_CUDA(cudaGetLastError());
   return MC_OK;
 }
@@ -179,36 +208,6 @@ NormShape norm_ring_shape(int64_t cols, int64_t row_bytes, int64_t q_row, int64_
   R->q_row = static_cast<int>(q_row);
   R->s_row = static_cast<int>(s_row);
   return n;
-}
-
-template <typename F>
-void with_nv(int nv, F&& f) {
-  if (nv == 1) f(std::integral_constant<int, 1>{});
-  else if (nv == 2) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 4>{});
-}
-template <typename F>
-void with_bool(bool b, F&& f) {
-  if (b) f(std::true_type{});
-  else f(std::false_type{});
-}
-// Bytes of an access that every row of `cols` elements begins on a boundary of.
-template <typename T, typename F>
-void with_width(int64_t cols, F&& f) {
-  if (cols * int64_t(sizeof(T)) % 16 == 0) f(std::integral_constant<int, 16>{});
-  else if (sizeof(T) == 4 || cols % 2 == 0) f(std::integral_constant<int, 4>{});
-  else f(std::integral_constant<int, int(sizeof(T))>{});
-}
-template <typename F>
-void with_fmt(int fmt, F&& f) {
-  if (fmt == MC_ACT_E4M3) f(std::integral_constant<int, ACT_E4M3>{});
-  else if (fmt == MC_ACT_INT8) f(std::integral_constant<int, ACT_INT8>{});
-  else f(std::integral_constant<int, ACT_NONE>{});
-}
-template <typename F>
-void with_dtype(int dtype, F&& f) {
-  if (dtype == MC_F32) f(float{});
-  else f(__nv_bfloat16{});
 }
 
 int check_norm(const void* w, int dtype, int w_dtype, int64_t rows, int64_t cols) {
@@ -377,7 +376,7 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
     if (x->fmt == MC_ACT_E4M3) go(act8_scatter_kernel<ACT_E4M3>);
     else go(act8_scatter_kernel<ACT_INT8>);
     MC_CUDA(cudaGetLastError());
-  } else if ((rc = unpack(*st, x, ws + p.off_x, MC_BF16, p.ldx, true, K_WGRAD_PREP, s)) != MC_OK) {
+  } else if ((rc = unpack(*st, x, ws + p.off_x, MC_BF16, p.ldx, K_WGRAD_PREP, s)) != MC_OK) {
     return rc;
   }
 
@@ -539,10 +538,10 @@ MC_API int mc_act8_pack(const void* x, int x_dtype, const mc_act8* a, void* stre
   ProfScope prof(K_ACT_PACK, s, 0, 0, double(a->rows) * a->cols * (dtype_bytes(x_dtype) + 1 + 1.0 / ACT_BLOCK));
   with_dtype(x_dtype, [&](auto t) {
     using T = decltype(t);
-    with_bool(a->cols % 8 == 0, [&](auto v) {
-      constexpr bool V = decltype(v)::value;
-      if (a->fmt == MC_ACT_E4M3) pack_launch<T, ACT_E4M3, V>(x, a, chunks, blocks, s);
-      else pack_launch<T, ACT_INT8, V>(x, a, chunks, blocks, s);
+    with_group(a->cols, [&](auto g) {
+      constexpr int G = decltype(g)::value;
+      if (a->fmt == MC_ACT_E4M3) pack_launch<T, ACT_E4M3, G>(x, a, chunks, blocks, s);
+      else pack_launch<T, ACT_INT8, G>(x, a, chunks, blocks, s);
     });
   });
   MC_CUDA(cudaGetLastError());
@@ -562,7 +561,7 @@ MC_API int mc_act8_unpack(const mc_act8* a, void* out, int out_dtype, void* stre
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   if ((rc = act_device_state(&st)) != MC_OK) return rc;
-  return unpack(*st, a, out, out_dtype, a->cols, a->cols % 8 == 0, K_ACT_UNPACK,
+  return unpack(*st, a, out, out_dtype, a->cols, K_ACT_UNPACK,
                 static_cast<cudaStream_t>(stream));
 }
 
@@ -622,15 +621,15 @@ MC_API int mc_rms_norm(const void* x, const void* residual, const void* w, int d
     a.eps = eps;
     a.inv_d = 1.0 / static_cast<double>(cols);
     with_fmt(y8 ? y8->fmt : -1, [&](auto f) {
-      with_bool(cols % 8 == 0, [&](auto v) {
+      with_group(cols, [&](auto g) {
         constexpr int F = decltype(f)::value;
-        constexpr bool V = decltype(v)::value;
+        constexpr int G = decltype(g)::value;
         if (sh.threads <= 256) {
-          with_nv(sh.nv, [&](auto nv) { rms_norm_kernel<T, F, V, decltype(nv)::value, 256><<<blocks, dim, 0, s>>>(a); });
+          with_nv(sh.nv, [&](auto nv) { rms_norm_kernel<T, F, G, decltype(nv)::value, 256><<<blocks, dim, 0, s>>>(a); });
         } else if (sh.nv == 1) {
-          rms_norm_kernel<T, F, V, 1, NORM_MAX_THREADS><<<blocks, dim, 0, s>>>(a);
+          rms_norm_kernel<T, F, G, 1, NORM_MAX_THREADS><<<blocks, dim, 0, s>>>(a);
         } else {
-          rms_norm_kernel<T, F, V, 4, NORM_MAX_THREADS><<<blocks, dim, 0, s>>>(a);
+          rms_norm_kernel<T, F, G, 4, NORM_MAX_THREADS><<<blocks, dim, 0, s>>>(a);
         }
       });
     });
@@ -742,11 +741,15 @@ MC_API int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, c
         };
         constexpr int F = decltype(f)::value;
         if (cols % 8 == 0) {  // rows too wide for the ring
-          launch(rms_norm_bwd_kernel<T, F, true, 4, NORM_MAX_THREADS>);
-        } else if (sh.threads > 256) {
-          launch(rms_norm_bwd_kernel<T, F, false, 4, NORM_MAX_THREADS>);
+          launch(rms_norm_bwd_kernel<T, F, 8, 4, NORM_MAX_THREADS>);
         } else {
-          with_nv(sh.nv, [&](auto nv) { launch(rms_norm_bwd_kernel<T, F, false, decltype(nv)::value, 256>); });
+          auto odd = [&](auto g) {
+            constexpr int G = decltype(g)::value;
+            if (sh.threads > 256) launch(rms_norm_bwd_kernel<T, F, G, 4, NORM_MAX_THREADS>);
+            else with_nv(sh.nv, [&](auto nv) { launch(rms_norm_bwd_kernel<T, F, G, decltype(nv)::value, 256>); });
+          };
+          if (cols % 2 == 0) odd(std::integral_constant<int, 2>{});
+          else odd(std::integral_constant<int, 1>{});
         }
       });
     });

@@ -61,15 +61,15 @@ __device__ __forceinline__ float scaled_to_odd(float xw, float r_hi, float r_lo)
 }
 
 // The norm's weight of one fragment (bf16 or fp32), 0 past D.
-template <bool VEC>
+template <int G>
 __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, int lane, int D, float (&v)[8]) {
   if (w_f32) {
     RawFrag<float> f;
-    load_frag<VEC>(f, static_cast<const float*>(w), c0, lane, D);
+    load_frag<G>(f, static_cast<const float*>(w), c0, lane, D);
     frag_floats(f, v);
   } else {
     RawFrag<__nv_bfloat16> f;
-    load_frag<VEC>(f, static_cast<const __nv_bfloat16*>(w), c0, lane, D);
+    load_frag<G>(f, static_cast<const __nv_bfloat16*>(w), c0, lane, D);
     frag_floats(f, v);
   }
 }
@@ -93,7 +93,7 @@ struct NormFwdArgs {
 // The sum of squares is kept in 64 bits beyond each fragment's eight terms: its
 // error would move every value of the row the same way.  (Every square in 64
 // bits: 115 us for 16384 x 4096 bf16 rows, bound by the conversions.)
-template <typename T, int FMT, bool VEC, int NV, int THREADS>
+template <typename T, int FMT, int G, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<T> a) {
   __shared__ double buf[32];
   // blockDim: {32 * warps of a row, rows}
@@ -105,15 +105,15 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<
   double sum = 0.0;
   if (live) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_frag<VEC>(f[j], a.x + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
+    for (int j = 0; j < NV; ++j) load_frag<G>(f[j], a.x + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
     if (a.r) {
       RawFrag<T> fr[NV];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) load_frag<VEC>(fr[j], a.r + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
+      for (int j = 0; j < NV; ++j) load_frag<G>(fr[j], a.r + base, (j * wpr + wr) * WARP_COLS, lane, a.D);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         frag_add(f[j], fr[j]);  // the norm sees h as the next layers will: in the stored type
-        store_raw<VEC>(a.h + base, (j * wpr + wr) * WARP_COLS, lane, a.D, f[j]);
+        store_raw<G>(a.h + base, (j * wpr + wr) * WARP_COLS, lane, a.D, f[j]);
       }
     }
 #pragma unroll
@@ -138,12 +138,12 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<
     if (c0 >= a.D) break;
     float v[8], w[8];
     frag_floats(f[j], v);
-    load_weight<VEC>(a.w, a.w_f32, c0, lane, a.D, w);
+    load_weight<G>(a.w, a.w_f32, c0, lane, a.D, w);
     // columns past D hold x = w = 0
     if constexpr (FMT == ACT_NONE) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * w[i];
-      store_frag<VEC>(a.y + base, c0, lane, a.D, v);
+      store_frag<G>(a.y + base, c0, lane, a.D, v);
     } else {
       if (sizeof(T) == 2 && !a.w_f32) {
 #pragma unroll
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i], w[i], rstd, r_lo);
       }
-      store_frag8<FMT, VEC>(a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D, v);
+      store_frag8<FMT, G>(a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D, v);
     }
   }
 }
@@ -190,7 +190,7 @@ struct NormBwdRaw<T, ACT_INT8> {
 // A block walks rows with a fixed step and keeps dw of its columns in
 // registers; the next row's loads are issued before this row's sum, so that
 // the memory stays busy across the block-wide reduction.
-template <typename T, int FMT, bool VEC, int NV, int THREADS>
+template <typename T, int FMT, int G, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs<T> a) {
   __shared__ float buf[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -212,13 +212,13 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
     for (int j = 0; j < NV; ++j) {
       const int c0 = (j * a.wpr + wr) * WARP_COLS;
       if (c0 >= a.D) break;
-      load_frag<VEC>(f[j].dy, a.dy + row * a.D, c0, lane, a.D);
+      load_frag<G>(f[j].dy, a.dy + row * a.D, c0, lane, a.D);
       if constexpr (FMT == ACT_NONE) {
-        load_frag<VEC>(f[j].h, a.h + row * a.D, c0, lane, a.D);
+        load_frag<G>(f[j].h, a.h + row * a.D, c0, lane, a.D);
       } else {
-        load_frag8<VEC>(f[j].h, a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D);
+        load_frag8<G>(f[j].h, a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D);
       }
-      if (a.dh) load_frag<VEC>(f[j].dh, a.dh + row * a.D, c0, lane, a.D);
+      if (a.dh) load_frag<G>(f[j].dh, a.dh + row * a.D, c0, lane, a.D);
     }
   };
   auto values = [&](const NormBwdRaw<T, FMT>& f, int c0, float rstd, float (&dy)[8], float (&xhat)[8]) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
     if constexpr (FMT == ACT_NONE) {
       frag_floats(f.h, xhat);
     } else {
-      frag8_floats<FMT, VEC>(f.h, c0, lane, a.D, xhat);
+      frag8_floats<FMT, G>(f.h, c0, lane, a.D, xhat);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) xhat[i] *= rstd;
@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
         if (c0 >= a.D) break;
         float dy[8], xhat[8], w[8];
         values(cur[j], c0, rstd, dy, xhat);
-        load_weight<VEC>(a.w, a.w_f32, c0, lane, a.D, w);
+        load_weight<G>(a.w, a.w_f32, c0, lane, a.D, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool in = frag_col<VEC>(c0, lane, i) < a.D;
+          const bool in = frag_col<G>(c0, lane, i) < a.D;
           const float p = in ? dy[i] * xhat[i] : 0.f;
           dw[j][i] += p;
           dot = fmaf(p, w[i], dot);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
         if (c0 >= a.D) break;
         float dy[8], xhat[8], w[8], o[8];
         values(cur[j], c0, rstd, dy, xhat);
-        load_weight<VEC>(a.w, a.w_f32, c0, lane, a.D, w);
+        load_weight<G>(a.w, a.w_f32, c0, lane, a.D, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = rstd * (dy[i] * w[i] - xhat[i] * c);
         if (a.dh) {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] += t[i];
         }
-        store_frag<VEC>(a.dx + row * a.D, c0, lane, a.D, o);
+        store_frag<G>(a.dx + row * a.D, c0, lane, a.D, o);
       }
     }
 #pragma unroll
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
     if (c0 >= a.D) break;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = frag_col<VEC>(c0, lane, i);
+      const int c = frag_col<G>(c0, lane, i);
       if (c < a.D) out[c] = dw[j][i];
     }
   }
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm
   float dw[NV][8], w[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_weight<true>(a.w, a.w_f32, (j * a.wpr + wr) * WARP_COLS, lane, a.D, w[j]);
+    load_weight<8>(a.w, a.w_f32, (j * a.wpr + wr) * WARP_COLS, lane, a.D, w[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
@@ -416,15 +416,15 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm
     live = live && got;
     auto values = [&](int c0, float (&dy)[8], float (&xhat)[8]) {
       RawFrag<T> f;
-      load_frag<true>(f, s_dy, c0, lane, a.D);
+      load_frag<8>(f, s_dy, c0, lane, a.D);
       frag_floats(f, dy);
       if constexpr (FMT == ACT_NONE) {
-        load_frag<true>(f, s_h, c0, lane, a.D);
+        load_frag<8>(f, s_h, c0, lane, a.D);
         frag_floats(f, xhat);
       } else {
         Raw8 q;
-        load_frag8<true>(q, s_q, s_s, c0, lane, a.D);
-        frag8_floats<FMT, true>(q, c0, lane, a.D, xhat);
+        load_frag8<8>(q, s_q, s_s, c0, lane, a.D);
+        frag8_floats<FMT, 8>(q, c0, lane, a.D, xhat);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) xhat[i] *= rstd;
@@ -470,12 +470,12 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm
         if (a.dh) {
           RawFrag<T> f;
           float t[8];
-          load_frag<true>(f, s_dh, c0, lane, a.D);
+          load_frag<8>(f, s_dh, c0, lane, a.D);
           frag_floats(f, t);
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] += t[i];
         }
-        store_frag<true>(a.dx + row * a.D, c0, lane, a.D, o);
+        store_frag<8>(a.dx + row * a.D, c0, lane, a.D, o);
       }
     }
     __syncwarp();
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm
   }
   float* out = a.partial + ((long long)blockIdx.x * groups + group) * a.D;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) store_frag<true>(out, (j * a.wpr + wr) * WARP_COLS, lane, a.D, dw[j]);
+  for (int j = 0; j < NV; ++j) store_frag<8>(out, (j * a.wpr + wr) * WARP_COLS, lane, a.D, dw[j]);
 }
 
 // dw[c] = sum of the partial rows, each column's in a fixed order: warp w of a

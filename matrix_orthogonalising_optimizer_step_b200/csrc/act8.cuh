@@ -291,6 +291,8 @@ __device__ __forceinline__ void frag8_floats(const Raw8& f, int c0, int lane, in
 }
 
 // -------------------------------------------------------------- pack, unpack
+// Bound by memory: 16384 x 14336 bf16 packed in 133 us (712 MB, 5.3 TB/s, with
+// two thirds of the issue slots taken) and unpacked in 116 us (6.1 TB/s).
 // Work items are (row, 256-column chunk) pairs, one per warp and step; a warp
 // takes UNROLL items at once so that their loads are in flight together.
 struct RowWalk {

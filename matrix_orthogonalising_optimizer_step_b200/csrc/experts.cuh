@@ -14,6 +14,9 @@
 // expert row read or written once, so the kernels go token by token through
 // `position` (reading x once for its K copies) and never through `source`.
 // Nothing is added atomically: every sum has one owner and a fixed order.
+// Measured on 4096 tokens of 8 pairs, 64 experts, 7168 bf16 columns: sort 12 us
+// (with about 4 us of the timing's own), gather 87 us (529 MB, 6.1 TB/s),
+// combine's gradient 167 us (998 MB, 6.0 TB/s).
 #pragma once
 
 #include "act8.cuh"
@@ -386,9 +389,9 @@ __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_kernel(const T* _
 // the last of their turns over the row's 512-byte runs) share the row, every
 // pair's dot product is kept by thread over the whole row and joined at the end
 // (lanes by a tree, then warps in order).  dy may be y itself: a thread reads what it overwrites.
-// Four pairs' loads are in flight at a time; more would cost the registers
-// that let three blocks share an SM (all eight at once: one block, 260 us for
-// 4096 tokens of 8 pairs of 7168 bf16 columns; so: see the launch's figure).
+// Four pairs' loads are in flight at a time: all eight (145 registers) left one
+// block an SM and took 273 us for the case above; eight or two at 3 or 4 blocks
+// an SM 199 and 193 us.
 constexpr int BACK_PAIRS = 8;  // pairs whose sums a pass over the row keeps
 constexpr int BACK_AHEAD = 4;  // pairs loaded together
 template <typename T, int W>

@@ -7,10 +7,13 @@
 //             dx = rstd (g - xhat mean(g xhat)) + dh,   dw = sum over rows of dy xhat
 //             (dh: gradient reaching h past the norm; h as stored, in 8 bits if it was kept so)
 //
-// Both are bound by memory: a row is read once, kept in registers between its
-// sum and its output, and written once.  `wpr` warps share a row (a warp holds
-// 256 columns per fragment, NV fragments), so a block of 8 warps takes 8 / wpr
-// rows; sums are fp32 trees of a fixed order.
+// Both are bound by memory: a row is read once, kept in registers (forward) or
+// shared memory (backward) between its sum and its output, and written once.
+// `wpr` warps share a row (a warp holds 256 columns per fragment, NV fragments),
+// so a block of 8 warps takes 8 / wpr rows; sums are trees of a fixed order.
+// Measured on 16384 x 4096 bf16 rows: forward with residual and e4m3 output 80 us
+// (472 MB, 5.9 TB/s of the 6.55 a copy reaches here), backward 95 us (537 MB, 5.7
+// TB/s) and under 8 us for the sum of dw's parts.
 #pragma once
 
 #include "act8.cuh"
@@ -304,6 +307,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) rms_norm_bwd_
 // twice from there, for the row's sum and for its output, so that what is in
 // flight does not depend on registers.  dw and the weight stay in registers.
 // A stage holds one row for each of the block's groups of `wpr` warps.
+// (The next row's loads in registers instead, as above: 137 us for the 95 us
+// case; 122 registers left two blocks an SM and half the bytes in flight.)
 struct NormRing {
   int stages, stage_bytes;
   int off_dh, off_h, off_s;             // of a stage's dh rows, h rows (or codes) and scale bytes (dy at 0)

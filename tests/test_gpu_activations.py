@@ -116,6 +116,38 @@ def test_pack_leaves_the_padding_and_takes_any_leading_shape():
     ok()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [256, 250, 251])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pack_of_any_bits(dtype, D, fmt):
+    """Random bit patterns: every exponent, subnormals, infinities and NaN."""
+    bits = torch.randint(-2 ** 31, 2 ** 31, (200, D), generator=gen(D), device=DEV, dtype=torch.int64).to(torch.int32)
+    bits[100:] = (bits[100:] & 0x007FFFFF) | (torch.randint(100, 140, (100, 1), generator=gen(1), device=DEV).to(torch.int32) << 23)
+    x = bits.view(F32) if dtype == F32 else (bits >> 16).to(torch.int16).view(BF)
+    x = x.contiguous()
+    a = mc.act8_pack(x, fmt)
+    want, scale = oa.act8(n64(x), fmt)
+    assert np.array_equal(a.scale.cpu().numpy()[:, :-(-D // 32)], scale)
+    got = values(a)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~np.isnan(got)], want[~np.isnan(want)])
+    out = n64(mc.act8_unpack(a, dtype=F32))
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
+    assert np.array_equal(out[~np.isnan(want)], want[~np.isnan(want)]) and np.array_equal(np.isnan(out), np.isnan(want))
+    ok()
+
+
+@pytest.mark.parametrize("D", [64, 66, 67])
+def test_residual_sum_of_any_bits(D):
+    """h = x + residual rounds as the fp32 sum does, whatever the two bf16 numbers."""
+    a, b = (torch.randint(-2 ** 15, 2 ** 15, (4000, D), generator=gen(s), device=DEV, dtype=torch.int32).to(torch.int16) for s in (1, 2))
+    b[:2000] = (b[:2000] & 0x7F) | (a[:2000] & 0x7F80) ^ (b[:2000] & 0x0780)      # near exponents too
+    x, r = a.contiguous().view(BF), b.contiguous().view(BF)
+    h = mc.rms_norm(x, torch.ones(D, dtype=BF, device=DEV), residual=r).h
+    want = (x.float() + r.float()).to(BF)
+    nan = torch.isnan(want)
+    assert torch.equal(nan, torch.isnan(h)) and torch.equal(h[~nan].view(torch.int16), want[~nan].view(torch.int16))
+
+
 def test_every_code_unpacks():
     codes = torch.arange(256, dtype=torch.int32, device=DEV).to(torch.uint8).repeat(9, 1).contiguous()
     scale = torch.zeros(9, 16, dtype=torch.uint8, device=DEV)

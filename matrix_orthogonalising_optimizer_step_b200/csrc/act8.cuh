@@ -314,6 +314,7 @@ template <typename T, int FMT, int G>
 __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                                 uint8_t* __restrict__ s, long long rows, int D,
                                                                 long long q_ld, long long s_ld, int chunks) {
+  griddep_launch_dependents();
   constexpr int UNROLL = 4;
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
                                                                   long long s_ld, long long out_ld, int chunks) {
   constexpr int UNROLL = 4;
   griddep_launch_dependents();  // a weight gradient's product may set itself up
+  griddep_wait();               // what wrote the codes may still run
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
   const long long first = (long long)blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);

@@ -63,6 +63,21 @@ int take_workspace(DeviceState* st, size_t need, void** ws, size_t bytes) {
   return own_workspace(*st, need, ws);
 }
 
+// A launch that may begin while the stream's previous kernel runs out; the
+// kernel waits for that one before it touches memory.
+template <typename... P, typename... A>
+void early_launch(void (*kernel)(P...), unsigned blocks, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  set_pdl(attr[0], true);
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ----------------------------------------------- run-time choices to constants
 template <typename F>
 void with_nv(int nv, F&& f) {
@@ -117,9 +132,9 @@ void pack_launch(const void* x, const mc_act8* a, int chunks, unsigned blocks, c
 template <typename T, int FMT, int G>
 void unpack_launch(const mc_act8* a, void* out, int64_t rows, int64_t out_ld, int chunks,
                    unsigned blocks, cudaStream_t s) {
-  act8_unpack_kernel<T, FMT, G><<<blocks, ACT_THREADS, 0, s>>>(
-      static_cast<const uint8_t*>(a->q), static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), rows,
-      static_cast<int>(a->cols), a->q_ld, a->s_ld, out_ld, chunks);
+  early_launch(act8_unpack_kernel<T, FMT, G>, blocks, ACT_THREADS, s, static_cast<const uint8_t*>(a->q),
+               static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), rows, static_cast<int>(a->cols), a->q_ld, a->s_ld,
+               out_ld, chunks);
 }
 
 // The rows of `a` to `out`, rows of out_ld elements.
@@ -877,8 +892,8 @@ MC_API int mc_expert_gather(const void* x, int dtype, int64_t tokens, int top_k,
     const int segments = static_cast<int>((cols + seg_cols - 1) / seg_cols);
     const unsigned blocks = item_blocks(tokens * segments, 1, MOVE_THREADS / 32, st->sms);
     with_width<T>(cols, [&](auto v) {
-      expert_gather_kernel<T, decltype(v)::value><<<blocks, MOVE_THREADS, 0, s>>>(static_cast<const T*>(x), position, static_cast<T*>(rows_out),
-                                                                                 tokens, top_k, static_cast<int>(cols), segments);
+      early_launch(expert_gather_kernel<T, decltype(v)::value>, blocks, MOVE_THREADS, s, static_cast<const T*>(x), position,
+                   static_cast<T*>(rows_out), tokens, top_k, static_cast<int>(cols), segments);
     });
   });
   MC_CUDA(cudaGetLastError());

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(THREADS) expert_place_kernel(const I* __restri
                                                                const int* __restrict__ totals, int* __restrict__ offsets,
                                                                int* __restrict__ source, int* __restrict__ position,
                                                                long long pairs, int E) {
+  griddep_launch_dependents();
   extern __shared__ int sort_smem[];
   constexpr int WARPS = THREADS / 32;
   const int n = E + 1;
@@ -301,6 +302,7 @@ template <typename T, int W>
 __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const T* __restrict__ x, const int* __restrict__ position,
                                                                      T* __restrict__ out, long long tokens, int K, int D,
                                                                      int segments) {
+  griddep_wait();  // the sort may still run
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (MOVE_THREADS / 32);
   const long long first = (long long)blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5);

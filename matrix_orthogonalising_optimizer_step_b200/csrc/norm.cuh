@@ -99,6 +99,7 @@ struct NormFwdArgs {
 template <typename T, int FMT, int G, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<T> a) {
   __shared__ double buf[32];
+  griddep_launch_dependents();
   // blockDim: {32 * warps of a row, rows}
   const int lane = threadIdx.x & 31, wr = threadIdx.x >> 5, wpr = blockDim.x >> 5;
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;

@@ -341,12 +341,14 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restr
   }
 }
 
-// The rows of an 8-bit activation to bf16 or fp32.
+// The rows of an 8-bit activation to bf16 or fp32.  Kernels that start while
+// the stream's previous one runs read memory that it may still be writing, so
+// none of their pointers is __restrict__: read-only loads are defined only for
+// data that does not change while the kernel lives.
 template <typename T, int FMT, int G>
-__global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t* __restrict__ q,
-                                                                  const uint8_t* __restrict__ s, T* __restrict__ out,
-                                                                  long long rows, int D, long long q_ld,
-                                                                  long long s_ld, long long out_ld, int chunks) {
+__global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t* q, const uint8_t* s, T* out, long long rows,
+                                                                  int D, long long q_ld, long long s_ld, long long out_ld,
+                                                                  int chunks) {
   constexpr int UNROLL = 4;
   griddep_launch_dependents();  // a weight gradient's product may set itself up
   griddep_wait();               // what wrote the codes may still run

@@ -299,10 +299,9 @@ __host__ __device__ constexpr int run_cols() { return 32 * move_elems<T>(); }  /
 
 constexpr int GATHER_RUNS = 4;
 template <typename T, int W>
-__global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const T* __restrict__ x, const int* __restrict__ position,
-                                                                     T* __restrict__ out, long long tokens, int K, int D,
+__global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const T* x, const int* position, T* out, long long tokens, int K, int D,
                                                                      int segments) {
-  griddep_wait();  // the sort may still run
+  griddep_wait();  // the sort, or what wrote x, may still run: no __restrict__, so no read-only loads
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (MOVE_THREADS / 32);
   const long long first = (long long)blockIdx.x * (MOVE_THREADS / 32) + (threadIdx.x >> 5);

@@ -499,12 +499,11 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS <= 256 ? 2 : 1) rms_norm
 // dw[c] = sum of the partial rows, each column's in a fixed order: warp w of a
 // block takes rows w, w + 16, ..., then the 16 sums are added in turn.
 constexpr int NORM_DW_WARPS = 16;
-__global__ void __launch_bounds__(NORM_DW_WARPS * 32) rms_norm_dw_kernel(const float* __restrict__ partial, float* __restrict__ dw,
-                                                                         int parts, int D) {
+__global__ void __launch_bounds__(NORM_DW_WARPS * 32) rms_norm_dw_kernel(const float* partial, float* dw, int parts, int D) {
   __shared__ float buf[NORM_DW_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  griddep_wait();  // launched while the walk still runs
+  griddep_wait();  // launched while the walk still runs: no __restrict__, so no read-only loads
   constexpr int AHEAD = 8;
   float t[AHEAD];
 #pragma unroll

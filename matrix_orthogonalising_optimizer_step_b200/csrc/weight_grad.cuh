@@ -547,23 +547,33 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
 // order.  A block takes JOIN_ROWS rows of one tile, four columns a thread.
 constexpr int JOIN_ROWS = 16;
 template <typename T>
-__global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict__ part, T* __restrict__ out, int M, int N,
-                                                         int tiles_m, int tiles_n, int band, int first_tile, int ranges, int add) {
+__global__ void __launch_bounds__(256) wgrad_join_kernel(const float* part, T* out, int M, int N, int tiles_m, int tiles_n,
+                                                         int band, int first_tile, int ranges, int add) {
   const int split = blockIdx.x / (BM / JOIN_ROWS), strip = blockIdx.x % (BM / JOIN_ROWS);
   int tm, tn;
   wgrad_tile(first_tile + split, tiles_m, tiles_n, band, tm, tn);
   const int cc = (threadIdx.x & 63) * 4, c = tn * MMA_N + cc;
   const float* p = part + (long long)split * ranges * (BM * MMA_N) + cc;
-  griddep_wait();
+  griddep_wait();  // the product may still run: no __restrict__, so no read-only loads
+  constexpr int ROWS = JOIN_ROWS / 4;  // of a thread; all their sums before the first store, which no load may pass
+  const int r0 = strip * JOIN_ROWS + (threadIdx.x >> 6);
+  float4 sum[ROWS];
 #pragma unroll
-  for (int i = 0; i < JOIN_ROWS; i += 4) {
-    const int rr = strip * JOIN_ROWS + i + (threadIdx.x >> 6), r = tm * BM + rr;
-    if (r >= M || c >= N) continue;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < ranges; ++k) {
+  for (int i = 0; i < ROWS; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < ranges; ++k) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int rr = r0 + 4 * i;
+      if (tm * BM + rr >= M || c >= N) continue;
       const float4 v = *reinterpret_cast<const float4*>(p + (long long)k * (BM * MMA_N) + rr * MMA_N);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      sum[i].x += v.x; sum[i].y += v.y; sum[i].z += v.z; sum[i].w += v.w;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = tm * BM + r0 + 4 * i;
+    if (r >= M || c >= N) continue;
+    const float4 s = sum[i];
     const float t[4] = {s.x, s.y, s.z, s.w};
     T* o = out + (long long)r * N + c;
     if (N % 4 == 0 && !add) {  // whole aligned words

@@ -207,6 +207,33 @@ def test_each_operator_alone_in_a_graph():
     ok()
 
 
+@pytest.mark.parametrize("D", [333, 1002, 4096])
+def test_what_follows_a_kernel_reads_what_it_wrote(D):
+    """Sums written over the residual and gathered at once; codes written over the
+    last ones and expanded at once; the same buffers every time."""
+    T, E = 1500, 6
+    x, w = draw(130, T, D), (1 + 0.1 * draw(131, D, dtype=F32)).to(BF)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(132)
+    plan = mc.expert_sort(torch.randint(0, E, (T, 2), generator=g, device=DEV), E)
+    buf, rows = torch.empty_like(x), torch.empty(2 * T, D, dtype=BF, device=DEV)
+    want, got = draw(133, T, D), []
+    buf.copy_(want)
+    code = mc.act8_empty((T, D), "e4m3", device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        mc.rms_norm(x, w, residual=buf, h_out=buf)
+        mc.expert_gather(buf, plan, out=rows)
+        mc.act8_pack(buf, "e4m3", out=code)
+        got.append((buf.clone(), rows.clone(), mc.act8_unpack(code)))
+    src = plan.source.long()
+    for h, r, u in got:
+        want = (want.float() + x.float()).to(BF)         # fp32 sum, rounded to bf16: h to the bit
+        assert torch.equal(h, want) and torch.equal(r, want[src // 2])
+        assert torch.equal(u, mc.act8_unpack(mc.act8_pack(want, "e4m3")))
+    ok()
+
+
 def test_another_stream_and_two_at_once():
     layers = [Layer(50, T=700), Layer(70, T=700)]
     want = [[t.clone() for t in a.run()] for a in layers]

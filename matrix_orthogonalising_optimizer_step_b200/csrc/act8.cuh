@@ -291,10 +291,16 @@ __device__ __forceinline__ void frag8_floats(const Raw8& f, int c0, int lane, in
 }
 
 // -------------------------------------------------------------- pack, unpack
-// Bound by memory: 16384 x 14336 bf16 packed in 133 us (712 MB, 5.3 TB/s, with
-// two thirds of the issue slots taken) and unpacked in 116 us (6.1 TB/s).
-// Work items are (row, 256-column chunk) pairs, one per warp and step; a warp
-// takes UNROLL items at once so that their loads are in flight together.
+// Bound by memory: 16384 x 14336 bf16 packed to e4m3 in 114 us and unpacked in 112 us
+// (712 MB: 6.24 and 6.37 TB/s of the 6.55 a copy reaches here).
+// Work items are (row, chunk of RUNS 256-column runs) pairs, one per warp and step; a
+// warp takes PACK_FRAGS / RUNS items at once, so that PACK_FRAGS runs' loads are in
+// flight together.  An item's runs share its addresses: with one run an item the
+// pack spent its issue slots on them (2^27 bf16 to e4m3: 82 us with one run, 74
+// with two, 70 with four; 16384 x 14336: 133 with one).  Runs past the row's end are idle (1280 columns: 82 us
+// with items of one or two runs, 88 with four), so RUNS is the largest of 4, 2, 1 that
+// leaves at most a quarter idle.
+constexpr int PACK_FRAGS = 4;
 struct RowWalk {
   long long row;
   int chunk;
@@ -310,12 +316,12 @@ __device__ __forceinline__ void walk_next(RowWalk& w, long long step_rows, int s
 
 constexpr int ACT_THREADS = 256;
 
-template <typename T, int FMT, int G>
+template <typename T, int FMT, int G, int RUNS>
 __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                                 uint8_t* __restrict__ s, long long rows, int D,
                                                                 long long q_ld, long long s_ld, int chunks) {
   griddep_launch_dependents();
-  constexpr int UNROLL = 4;
+  constexpr int UNROLL = PACK_FRAGS / RUNS;
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
   const long long first = (long long)blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);
@@ -324,19 +330,30 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restr
   RowWalk w{first / chunks, static_cast<int>(first % chunks)};
   while (w.row < rows) {
     RowWalk at[UNROLL];
-    RawFrag<T> f[UNROLL];
+    RawFrag<T> f[UNROLL][RUNS];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       at[u] = w;
-      if (w.row < rows) load_frag<G>(f[u], x + w.row * D, w.chunk * WARP_COLS, lane, D);
+      if (w.row < rows) {
+        const T* xr = x + w.row * D;
+        const int c0 = w.chunk * (RUNS * WARP_COLS);
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) load_frag<G>(f[u][j], xr, c0 + j * WARP_COLS, lane, D);
+      }
       walk_next(w, step_rows, step_chunks, chunks);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       if (at[u].row >= rows) break;
-      float v[8];
-      frag_floats(f[u], v);
-      store_frag8<FMT, G>(q + at[u].row * q_ld, s + at[u].row * s_ld, at[u].chunk * WARP_COLS, lane, D, v);
+      uint8_t* qr = q + at[u].row * q_ld;
+      uint8_t* sr = s + at[u].row * s_ld;
+      const int c0 = at[u].chunk * (RUNS * WARP_COLS);
+#pragma unroll
+      for (int j = 0; j < RUNS; ++j) {
+        float v[8];
+        frag_floats(f[u][j], v);
+        store_frag8<FMT, G>(qr, sr, c0 + j * WARP_COLS, lane, D, v);
+      }
     }
   }
 }
@@ -345,11 +362,11 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_pack_kernel(const T* __restr
 // the stream's previous one runs read memory that it may still be writing, so
 // none of their pointers is __restrict__: read-only loads are defined only for
 // data that does not change while the kernel lives.
-template <typename T, int FMT, int G>
+template <typename T, int FMT, int G, int RUNS>
 __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t* q, const uint8_t* s, T* out, long long rows,
                                                                   int D, long long q_ld, long long s_ld, long long out_ld,
                                                                   int chunks) {
-  constexpr int UNROLL = 4;
+  constexpr int UNROLL = PACK_FRAGS / RUNS;
   griddep_launch_dependents();  // a weight gradient's product may set itself up
   griddep_wait();               // what wrote the codes may still run
   const int lane = threadIdx.x & 31;
@@ -360,19 +377,30 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
   RowWalk w{first / chunks, static_cast<int>(first % chunks)};
   while (w.row < rows) {
     RowWalk at[UNROLL];
-    Raw8 f[UNROLL];
+    Raw8 f[UNROLL][RUNS];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       at[u] = w;
-      if (w.row < rows) load_frag8<G>(f[u], q + w.row * q_ld, s + w.row * s_ld, w.chunk * WARP_COLS, lane, D);
+      if (w.row < rows) {
+        const uint8_t* qr = q + w.row * q_ld;
+        const uint8_t* sr = s + w.row * s_ld;
+        const int c0 = w.chunk * (RUNS * WARP_COLS);
+#pragma unroll
+        for (int j = 0; j < RUNS; ++j) load_frag8<G>(f[u][j], qr, sr, c0 + j * WARP_COLS, lane, D);
+      }
       walk_next(w, step_rows, step_chunks, chunks);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       if (at[u].row >= rows) break;
-      float v[8];
-      frag8_floats<FMT, G>(f[u], at[u].chunk * WARP_COLS, lane, D, v);
-      store_frag<G>(out + at[u].row * out_ld, at[u].chunk * WARP_COLS, lane, D, v);
+      T* o = out + at[u].row * out_ld;
+      const int c0 = at[u].chunk * (RUNS * WARP_COLS);
+#pragma unroll
+      for (int j = 0; j < RUNS; ++j) {
+        float v[8];
+        frag8_floats<FMT, G>(f[u][j], c0 + j * WARP_COLS, lane, D, v);
+        store_frag<G>(o, c0 + j * WARP_COLS, lane, D, v);
+      }
     }
   }
 }

@@ -114,8 +114,8 @@ void with_dtype(int dtype, F&& f) {
 // ------------------------------------------------------------ pack, unpack
 // Blocks for `items` warp items, `per` of them per warp and step: at most 32 a
 // SM, and every block as many steps.  More blocks than an SM holds at once (4 or
-// 5) even out the SMs' speeds: 16384 x 14336 unpacked with 8 a SM 126 us, with
-// 32 116 us, with one block per step 120 us.
+// 5) even out the SMs' speeds: 16384 x 14336 unpacked by items of one run with 8
+// a SM 126 us, with 32 116 us, with one block per step 120 us.
 unsigned item_blocks(long long items, int per, int warps, int sms) {
   const long long step = (long long)per * warps;
   const long long want = (items + step - 1) / step, most = 32LL * sms;
@@ -123,26 +123,42 @@ unsigned item_blocks(long long items, int per, int warps, int sms) {
   return static_cast<unsigned>(std::max<long long>(1, (want + steps - 1) / steps));
 }
 
+// Items of 4, 2 or 1 runs of 256 columns (see the kernels): f(runs, chunks a row, blocks).
+template <typename F>
+void with_runs(int64_t rows, int64_t cols, int sms, F&& f) {
+  const int n = static_cast<int>((cols + WARP_COLS - 1) / WARP_COLS);
+  auto take = [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    const int chunks = (n + R - 1) / R;
+    f(r, chunks, item_blocks(rows * chunks, PACK_FRAGS / R, ACT_THREADS / 32, sms));
+  };
+  auto fits = [&](int r) { return 4 * n >= 3 * r * ((n + r - 1) / r); };
+  if (fits(4)) take(std::integral_constant<int, 4>{});
+  else if (fits(2)) take(std::integral_constant<int, 2>{});
+  else take(std::integral_constant<int, 1>{});
+}
+
 template <typename T, int FMT, int G>
-void pack_launch(const void* x, const mc_act8* a, int chunks, unsigned blocks, cudaStream_t s) {
-  act8_pack_kernel<T, FMT, G><<<blocks, ACT_THREADS, 0, s>>>(
+void pack_launch(const void* x, const mc_act8* a, int sms, cudaStream_t s) {
+  with_runs(a->rows, a->cols, sms, [&](auto r, int chunks, unsigned blocks) {
+    act8_pack_kernel<T, FMT, G, decltype(r)::value><<<blocks, ACT_THREADS, 0, s>>>(
       static_cast<const T*>(x), static_cast<uint8_t*>(a->q), static_cast<uint8_t*>(a->scale), a->rows,
       static_cast<int>(a->cols), a->q_ld, a->s_ld, chunks);
+  });
 }
 template <typename T, int FMT, int G>
-void unpack_launch(const mc_act8* a, void* out, int64_t rows, int64_t out_ld, int chunks,
-                   unsigned blocks, cudaStream_t s) {
-  early_launch(act8_unpack_kernel<T, FMT, G>, blocks, ACT_THREADS, s, static_cast<const uint8_t*>(a->q),
-               static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), rows, static_cast<int>(a->cols), a->q_ld, a->s_ld,
-               out_ld, chunks);
+void unpack_launch(const mc_act8* a, void* out, int64_t out_ld, int sms, cudaStream_t s) {
+  with_runs(a->rows, a->cols, sms, [&](auto r, int chunks, unsigned blocks) {
+    early_launch(act8_unpack_kernel<T, FMT, G, decltype(r)::value>, blocks, ACT_THREADS, s, static_cast<const uint8_t*>(a->q),
+                 static_cast<const uint8_t*>(a->scale), static_cast<T*>(out), a->rows, static_cast<int>(a->cols), a->q_ld,
+                 a->s_ld, out_ld, chunks);
+  });
 }
 
 // The rows of `a` to `out`, rows of out_ld elements.
 int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, int64_t out_ld, int kind, cudaStream_t s) {
   const int64_t rows = a->rows;
   if (rows == 0) return MC_OK;
-  const int chunks = static_cast<int>((a->cols + WARP_COLS - 1) / WARP_COLS);
-  const unsigned blocks = item_blocks(rows * chunks, 4, ACT_THREADS / 32, st.sms);
   const bool e4 = a->fmt == MC_ACT_E4M3;
   ProfScope prof(kind, s, 0, 0, double(rows) * a->cols * (dtype_bytes(dtype) + 1 + 1.0 / ACT_BLOCK));
   with_dtype(dtype, [&](auto t) {
@@ -150,8 +166,8 @@ int unpack(const DeviceState& st, const mc_act8* a, void* out, int dtype, int64_
     // rows of `out` may be padded to whole words, which are then written whole
     with_group(out_ld % 8 == 0 ? 8 : a->cols, [&](auto g) {
       constexpr int G = decltype(g)::value;
-      if (e4) unpack_launch<T, ACT_E4M3, G>(a, out, rows, out_ld, chunks, blocks, s);
-      else unpack_launch<T, ACT_INT8, G>(a, out, rows, out_ld, chunks, blocks, s);
+      if (e4) unpack_launch<T, ACT_E4M3, G>(a, out, out_ld, st.sms, s);
+      else unpack_launch<T, ACT_INT8, G>(a, out, out_ld, st.sms, s);
     });
   });
   MC_CUDA(cudaGetLastError());
@@ -548,15 +564,13 @@ MC_API int mc_act8_pack(const void* x, int x_dtype, const mc_act8* a, void* stre
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   if ((rc = act_device_state(&st)) != MC_OK) return rc;
-  const int chunks = static_cast<int>((a->cols + WARP_COLS - 1) / WARP_COLS);
-  const unsigned blocks = item_blocks(a->rows * chunks, 4, ACT_THREADS / 32, st->sms);
   ProfScope prof(K_ACT_PACK, s, 0, 0, double(a->rows) * a->cols * (dtype_bytes(x_dtype) + 1 + 1.0 / ACT_BLOCK));
   with_dtype(x_dtype, [&](auto t) {
     using T = decltype(t);
     with_group(a->cols, [&](auto g) {
       constexpr int G = decltype(g)::value;
-      if (a->fmt == MC_ACT_E4M3) pack_launch<T, ACT_E4M3, G>(x, a, chunks, blocks, s);
-      else pack_launch<T, ACT_INT8, G>(x, a, chunks, blocks, s);
+      if (a->fmt == MC_ACT_E4M3) pack_launch<T, ACT_E4M3, G>(x, a, st->sms, s);
+      else pack_launch<T, ACT_INT8, G>(x, a, st->sms, s);
     });
   });
   MC_CUDA(cudaGetLastError());

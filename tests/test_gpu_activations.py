@@ -88,6 +88,19 @@ def test_pack_at_the_ends_of_the_range(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [8, 249, 512, 510, 511, 600, 1024, 1030, 1276, 1277, 1280, 2300, 2301, 2304, 5000])
+def test_pack_of_one_to_many_runs_a_row(D, fmt):
+    """Rows of 1 to 20 runs of 256 columns, whole and not, in all three column layouts."""
+    x = draw(D, 150, D)
+    a = mc.act8_pack(x, fmt)
+    want, scale = oa.act8(n64(x), fmt)
+    assert np.array_equal(a.scale.cpu().numpy()[:, :-(-D // 32)], scale)
+    assert np.array_equal(values(a), want)
+    assert np.array_equal(n64(mc.act8_unpack(a)), want) and np.array_equal(n64(mc.act8_unpack(a, dtype=F32)), want)
+    ok()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("D", [96, 97, 98])
 def test_a_nan_or_infinity_costs_its_block_alone(fmt, D):
     x = draw(5, 6, D)

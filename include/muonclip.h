@@ -542,10 +542,11 @@ int mc_rms_norm_backward(const void* dy, const void* dh, const void* h, const mc
  * mc_weight_grad -- the gradient of an nn.Linear weight (rows = out-features)
  * from its output's gradient and its input kept in 8 bits:
  *   g[m][n] = sum over rows r of dy[r][m] * x[r][n]        (accumulate: added to g)
- * on tensor cores, with x's values exact in bf16 and fp32 accumulation.  For an
- * fp32 g, sums are carried over 1024 rows inside the tensor cores and added
- * beyond that with rounding to nearest, in a fixed order.  Results depend on
- * nothing but the operands and their sizes.
+ * on tensor cores, with x's values exact in bf16 and fp32 accumulation: sums are
+ * carried over 1024 rows (2048 for a bf16 g) inside the tensor cores, which cut
+ * toward zero (2^-23 of the sum per 16 rows), and added beyond that in fp32 with
+ * rounding to nearest, in a fixed order; a bf16 g is rounded once more.  Results
+ * depend on nothing but the operands and their sizes.
  * dy     device bf16, x->rows x out_features
  * g      device, out_features x x->cols, g_dtype; accumulate needs MC_F32
  * x->rows == 0 gives g = 0 (accumulate: unchanged).

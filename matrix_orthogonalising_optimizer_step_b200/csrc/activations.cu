@@ -252,8 +252,12 @@ int check_norm(const void* w, int dtype, int w_dtype, int64_t rows, int64_t cols
 }
 
 // ------------------------------------------------------------ weight gradient
-// Longest contraction one accumulator takes for an fp32 output.
+// Longest contraction one accumulator takes, in k-blocks, for an fp32 and for a
+// bf16 output.  14336 x 4096 from 16384 rows to bf16: 1461 us with one accumulator,
+// 1474 with chunks of 32 k-blocks, 1487 with 16; entries that are not the rounded
+// formula's: 0.34 %, 0.044 %, 0.023 % (a fp32 matrix product: 0.033 %).
 constexpr int kWgradChunkKb = 16;
+constexpr int kWgradChunkKbBf16 = 32;
 
 struct WgradPlan {
   int64_t ldx, ldy;          // rows of the bf16 X and of dY
@@ -418,7 +422,7 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
   P.out = g;
   P.out_f32 = g_dtype == MC_F32 ? 1 : 0;
   P.add = accumulate ? 1 : 0;
-  P.chunk_kb = P.out_f32 ? kWgradChunkKb : INT_MAX / 2;
+  P.chunk_kb = P.out_f32 ? kWgradChunkKb : kWgradChunkKbBf16;
   P.tiles_m = static_cast<int>((M + BM - 1) / BM);
   P.tiles_n = static_cast<int>((N + MMA_N - 1) / MMA_N);
   P.band = 8;

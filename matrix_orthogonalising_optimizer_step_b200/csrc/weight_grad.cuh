@@ -29,10 +29,12 @@
 // go to scratch and are joined by one more launch, in order (4096 x 4096 from 8192
 // rows is 256 tiles for 74 pairs, 3.46 waves: see wgrad_plan for the figures).
 //
-// fp32 outputs: the tensor cores' own fp32 additions lose up to a unit in the
-// last place per step, always toward zero, so an accumulator takes at most
-// `chunk_kb` k-blocks; the epilogue threads add the chunks in registers, rounding
-// to nearest, and store once.
+// The tensor cores' own fp32 additions lose up to a unit in the last place per
+// step, always toward zero, so an accumulator takes at most `chunk_kb` k-blocks; the
+// epilogue threads add the chunks in registers, rounding to nearest, and round
+// once more for a bf16 output.  (One accumulator for the whole contraction of a
+// bf16 output, as if its rounding hid the rest: from 16384 rows 0.34 % of the
+// rounded entries were not those of the formula; an fp32 product: 0.03 %.)
 #pragma once
 
 #include "umma_gemm.cuh"
@@ -456,73 +458,71 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) weight_grad_kernel(const __gr
         }
         continue;
       }
-      if constexpr (F32) {
-        // every chunk's columns into this thread's sums (its row's WCOLS columns)
-        float sum[WCOLS];
-#pragma unroll
-        for (int j = 0; j < WCOLS; ++j) sum[j] = 0.f;
-        for (int c0 = 0; c0 < it.num_kb; c0 += P.chunk_kb) {
-          // every lane waits; the warp goes on only if all of them saw the phase complete
-          const bool got = wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, P.err);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * T::N + half * WCOLS;
-#pragma unroll
-          for (int cb = 0; cb < WCOLS; cb += 16) {
-            float v[16];
-            tmem_ld16(t_row + cb, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[cb + j] += v[j];
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
-          if (++acc == NACC) {
-            acc = 0;
-            acc_phase ^= 1;
-          }
-        }
-        if (ok && r0 < P.M) {
-#pragma unroll
-          for (int cb = 0; cb < WCOLS; cb += COLS) {
-            if (cbase + cb >= P.N) continue;
-            if (it.part >= 0) {
-              wgrad_tma_out<true>(&P.map_p, half * WCOLS + cb, HALF * static_cast<int>(rank) + q * 32, it.part, lane, buf, sum + cb, false);
-            } else {
-              wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, sum + cb, P.add != 0);
-            }
-          }
-        }
-      } else {
-        // bf16: one chunk (its rounding hides the accumulator's)
+      if (!F32 && it.num_kb <= P.chunk_kb && it.part < 0) {
+        // one chunk has no sums to hold: half of the columns is stored before the other
+        // half is read (64 experts' 2048 x 7168 from 32768 rows: 1076 us with this path,
+        // 1088 through the sums)
         const bool got = wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, P.err);
         if (!__all_sync(0xffffffffu, got)) break;
         tc_fence_after();
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * T::N + half * WCOLS;
 #pragma unroll
-        for (int cb = 0; cb < WCOLS; cb += COLS) {
-          float v[COLS];
+        for (int cb = 0; cb < WCOLS; cb += 64) {
+          float v[64];
           tmem_ld64(t_row + cb, v);
-          if (cb + COLS == WCOLS) {  // the accumulator is in registers: the next tile may have it
+          if (cb + 64 == WCOLS) {  // the accumulator is in registers: the next tile may have it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
           }
-          if (r0 >= P.M || cbase + cb >= P.N) continue;
-          if (it.part >= 0) {
-            const int pr = HALF * static_cast<int>(rank) + q * 32, pc = half * WCOLS + cb;
-            wgrad_tma_out<true>(&P.map_p, pc, pr, it.part, lane, buf, v, false);
-            wgrad_tma_out<true>(&P.map_p, pc + 32, pr, it.part, lane, buf, v + 32, false);
-          } else {
-            wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
-          }
+          if (r0 < P.M && cbase + cb < P.N) wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, v, false);
         }
         if (++acc == NACC) {
           acc = 0;
           acc_phase ^= 1;
+        }
+        continue;
+      }
+      // every chunk's columns into this thread's sums (its row's WCOLS columns)
+      float sum[WCOLS];
+#pragma unroll
+      for (int j = 0; j < WCOLS; ++j) sum[j] = 0.f;
+      for (int c0 = 0; c0 < it.num_kb; c0 += P.chunk_kb) {
+        // every lane waits; the warp goes on only if all of them saw the phase complete
+        const bool got = wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, P.err);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * T::N + half * WCOLS;
+#pragma unroll
+        for (int cb = 0; cb < WCOLS; cb += 16) {
+          float v[16];
+          tmem_ld16(t_row + cb, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[cb + j] += v[j];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
+        if (++acc == NACC) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (ok && r0 < P.M) {
+#pragma unroll
+        for (int cb = 0; cb < WCOLS; cb += COLS) {
+          if (cbase + cb >= P.N) continue;
+          if (it.part >= 0) {
+#pragma unroll
+            for (int h = 0; h < COLS; h += 32)
+              wgrad_tma_out<true>(&P.map_p, half * WCOLS + cb + h, HALF * static_cast<int>(rank) + q * 32, it.part, lane, buf, sum + cb + h,
+                                  false);
+          } else {
+            wgrad_store<F32>(P, it.prob, r0, cbase + cb, lane, buf, sum + cb, F32 && P.add != 0);
+          }
         }
       }
     }

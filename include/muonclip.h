@@ -560,14 +560,16 @@ int mc_weight_grad(const void* dy, const mc_act8* x, int64_t out_features, void*
  * mc_expert_weight_grad -- mc_weight_grad of every expert's weight in one call:
  *   g[e][m][n] = sum over rows r in [offsets[e], offsets[e + 1]) of dy[r][m] * x[row(r)][n]
  * dy       device bf16, rows x out_features, rows sorted by expert (mc_expert_sort)
- * x        position NULL: row(r) = r, x has `rows` rows, sorted like dy; else x has
+ * x        position NULL: row(r) = r, every row of an expert's range counts, x has
+ *          `rows` rows, sorted like dy; else x has
  *          rows / top_k rows in token order, and row(position[t][k]) = t
  * offsets, position  device int32 [experts + 1] and [rows / top_k][top_k], of one
  *          mc_expert_sort; offsets are taken into [0, rows] and entries of position
- *          outside it count as dropped
+ *          outside it count as dropped, also where they were set so after the sort
  * g        device, experts x out_features x x->cols, g_dtype; accumulate needs MC_F32.
  *          An expert without rows gets zeros (accumulate: is left as it is).
- * Rows of dy outside every expert are not read into any result, whatever they hold.
+ * Rows of dy outside every expert and, with position, rows that no pair has, add
+ * nothing to any result, whatever they hold.
  * experts, top_k  at most 1024
  * workspace  >= mc_expert_weight_grad_workspace_size(...), or NULL.
  */

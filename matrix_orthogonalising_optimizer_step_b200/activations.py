@@ -481,7 +481,10 @@ def expert_weight_grad(dy, x: Act8, plan: ExpertPlan, *, gather: bool, dtype=Non
     """Gradients [E, out-features, in-features] of every expert's weight (see
     mc_expert_weight_grad) from dy bf16 [T * K, out-features] in sorted rows and
     x in 8 bits: in token order (``gather`` true: [T, in-features], e.g. the
-    input of the experts' first products) or sorted like dy (``gather`` false)."""
+    input of the experts' first products) or sorted like dy (``gather`` false).
+    With ``gather``, pairs whose ``plan.position`` was set outside the rows after
+    the sort add nothing, whatever their rows of dy hold; without, every row of
+    an expert's range counts as it is."""
     lib = load_library()
     T, K = _plan_pairs(plan)
     _plan_part(plan.offsets, "plan.offsets")

@@ -408,15 +408,16 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_unpack_kernel(const uint8_t*
 // Rows in token order to their pairs' sorted rows in bf16: output row
 // position[t * top_k + k] is row t, for every pair that is not dropped.  A token's
 // codes are read and converted once for all its rows.  out_ld is a multiple of
-// 8 and the bytes up to it may be written, whatever D.
+// 8 and the bytes up to it may be written, whatever D.  `reached`, zeros before,
+// gets a 1 for each row that a pair has.
 template <int FMT>
 __global__ void __launch_bounds__(ACT_THREADS) act8_scatter_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
-                                                                   __nv_bfloat16* __restrict__ out,
+                                                                   __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ reached,
                                                                    const int* __restrict__ position, int top_k, long long tokens,
                                                                    int D, long long q_ld, long long s_ld, long long out_ld,
                                                                    int segments) {
   constexpr int RUNS = 4;  // 256-column runs of an item
-  griddep_launch_dependents();  // the product may set itself up
+  griddep_launch_dependents();  // the maps' kernel may set itself up
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * (ACT_THREADS / 32);
   const long long first = (long long)blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);
@@ -443,6 +444,7 @@ __global__ void __launch_bounds__(ACT_THREADS) act8_scatter_kernel(const uint8_t
       for (int k = 0; k < kn; ++k) {
         const int r = __shfl_sync(0xffffffffu, mine, k);
         if (r < 0 || r >= rows) continue;
+        if (w.chunk == 0 && lane == 0) reached[r] = 1;
 #pragma unroll
         for (int u = 0; u < RUNS; ++u) {
           const int c = c0 + u * WARP_COLS + 8 * lane;

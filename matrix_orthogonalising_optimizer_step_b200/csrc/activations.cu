@@ -264,7 +264,7 @@ struct WgradPlan {
   int64_t tiles, split;      // one weight: tiles in all, those of them whose contraction is split
   int ranges, kb_range;      // into so many ranges of so many k-blocks
   bool copy_dy;
-  size_t off_x, off_dy, off_part, off_maps, off_ranges, total;
+  size_t off_x, off_dy, off_part, off_maps, off_ranges, off_reached, total;
 };
 
 // CTA pairs that the plan counts on; the launch takes what the device has.
@@ -309,10 +309,12 @@ WgradPlan wgrad_plan(int64_t rows, int64_t M, int64_t N, int experts) {
     return o;
   };
   p.off_x = take(size_t(rows) * p.ldx * 2);
-  p.off_dy = take(p.copy_dy ? size_t(rows) * p.ldy * 2 : 0);
+  // experts: room for dY without the rows that no pair has, too
+  p.off_dy = take(p.copy_dy || experts > 0 ? size_t(rows) * p.ldy * 2 : 0);
   p.off_part = take(size_t(p.split) * p.ranges * BM * MMA_N * 4);
   p.off_maps = take(size_t(experts) * 2 * sizeof(CUtensorMap));
-  p.off_ranges = take(size_t(experts) * sizeof(int2));
+  p.off_ranges = take(size_t(experts) * sizeof(int4));
+  p.off_reached = take(experts > 0 ? size_t(rows) : 0);
   p.total = at + 256;  // the parts start at the first 256-byte boundary (tensor maps need 128)
   return p;
 }
@@ -379,6 +381,21 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
   std::memset(&P, 0, sizeof(P));
   if ((rc = map_rows(&P.map_a, a, rows, M, p.ldy)) != MC_OK) return rc;
   if ((rc = map_rows(&P.map_b, ws + p.off_x, rows, N, p.ldx)) != MC_OK) return rc;
+  // rows of the workspace are padded to whole 16 bytes, so the 8-bit rows always take the wide path
+  if (position) {
+    const int segments = static_cast<int>((N + 4 * WARP_COLS - 1) / (4 * WARP_COLS));
+    const unsigned blocks = item_blocks(x->rows * segments, 1, ACT_THREADS / 32, st->sms);
+    MC_CUDA(cudaMemsetAsync(ws + p.off_reached, 0, size_t(rows), s));
+    ProfScope prof(K_WGRAD_PREP, s, 0, 0, double(x->rows) * N * (1 + 1.0 / ACT_BLOCK) + 2.0 * double(rows) * N);
+    auto go = [&](auto kernel) {
+      kernel<<<blocks, ACT_THREADS, 0, s>>>(static_cast<const uint8_t*>(x->q), static_cast<const uint8_t*>(x->scale),
+                                            reinterpret_cast<__nv_bfloat16*>(ws + p.off_x), ws + p.off_reached, position, top_k, x->rows,
+                                            static_cast<int>(N), x->q_ld, x->s_ld, p.ldx, segments);
+    };
+    if (x->fmt == MC_ACT_E4M3) go(act8_scatter_kernel<ACT_E4M3>);
+    else go(act8_scatter_kernel<ACT_INT8>);
+    MC_CUDA(cudaGetLastError());
+  }
   if (offsets) {
     WgradMapsParams mp;
     std::memset(&mp, 0, sizeof(mp));
@@ -386,34 +403,28 @@ int weight_grad(const void* dy, int64_t rows, const mc_act8* x, const int* offse
     mp.map_b = P.map_b;
     mp.offsets = offsets;
     mp.a = static_cast<const uint8_t*>(a);
+    mp.a_patched = ws + p.off_dy;
     mp.b = ws + p.off_x;
     mp.a_row_bytes = p.ldy * 2;
     mp.b_row_bytes = p.ldx * 2;
+    mp.reached = position ? ws + p.off_reached : nullptr;
     mp.maps = reinterpret_cast<CUtensorMap*>(ws + p.off_maps);
-    mp.ranges = reinterpret_cast<int2*>(ws + p.off_ranges);
+    mp.ranges = reinterpret_cast<int4*>(ws + p.off_ranges);
     mp.rows = static_cast<int>(rows);
-    ProfScope prof(K_WGRAD_PREP, s);
-    wgrad_maps_kernel<<<experts, 32, 0, s>>>(mp);
-    MC_CUDA(cudaGetLastError());
+    {
+      ProfScope prof(K_WGRAD_PREP, s);
+      early_launch(wgrad_maps_kernel, static_cast<unsigned>(experts), MAPS_THREADS, s, mp);
+      MC_CUDA(cudaGetLastError());
+    }
+    if (position) {
+      ProfScope prof(K_WGRAD_PREP, s);
+      early_launch(wgrad_patch_kernel, static_cast<unsigned>(2 * st->sms), MAPS_THREADS, s, mp, experts);
+      MC_CUDA(cudaGetLastError());
+    }
     P.maps = mp.maps;
     P.ranges_of = mp.ranges;
   }
-  // rows of the workspace are padded to whole 16 bytes, so this always takes the wide path
-  if (position) {
-    const int segments = static_cast<int>((N + 4 * WARP_COLS - 1) / (4 * WARP_COLS));
-    const unsigned blocks = item_blocks(x->rows * segments, 1, ACT_THREADS / 32, st->sms);
-    ProfScope prof(K_WGRAD_PREP, s, 0, 0, double(x->rows) * N * (1 + 1.0 / ACT_BLOCK) + 2.0 * double(rows) * N);
-    auto go = [&](auto kernel) {
-      kernel<<<blocks, ACT_THREADS, 0, s>>>(static_cast<const uint8_t*>(x->q), static_cast<const uint8_t*>(x->scale),
-                                            reinterpret_cast<__nv_bfloat16*>(ws + p.off_x), position, top_k, x->rows,
-                                            static_cast<int>(N), x->q_ld, x->s_ld, p.ldx, segments);
-    };
-    if (x->fmt == MC_ACT_E4M3) go(act8_scatter_kernel<ACT_E4M3>);
-    else go(act8_scatter_kernel<ACT_INT8>);
-    MC_CUDA(cudaGetLastError());
-  } else if ((rc = unpack(*st, x, ws + p.off_x, MC_BF16, p.ldx, K_WGRAD_PREP, s)) != MC_OK) {
-    return rc;
-  }
+  if (!position && (rc = unpack(*st, x, ws + p.off_x, MC_BF16, p.ldx, K_WGRAD_PREP, s)) != MC_OK) return rc;
 
   P.M = static_cast<int>(M);
   P.N = static_cast<int>(N);

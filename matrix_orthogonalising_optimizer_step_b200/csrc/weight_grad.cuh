@@ -46,7 +46,7 @@ struct WgradParams {
   CUtensorMap map_o;          // output [count][M][N]: boxes of 32 rows x 128 bytes
   CUtensorMap map_p;          // partial products [split items][256][256] fp32: boxes of 32 x 32
   const CUtensorMap* maps;    // experts: [2 * count] maps of dY's and X's rows of each, else null
-  const int2* ranges_of;      // experts: {first row, rows} of each
+  const int4* ranges_of;      // experts: {first row, rows, ..} of each
   void* out;
   long long out_bs;           // elements from one problem's output to the next
   int items;                  // work items: whole tiles, then the ranges of the split ones
@@ -81,33 +81,57 @@ __device__ __forceinline__ void tmap_acquire(const CUtensorMap* m) {
 }
 
 // ------------------------------------------------------------ experts' maps
-// One warp per expert: its row range from the offsets (clamped, so that no
-// offsets can reach outside the `rows` rows of the operands), and the two
-// tensor maps of these rows, copies of the whole operands' maps with another
-// base address and row extent.
+// One block per expert: its row range from the offsets (clamped, so that no
+// offsets can reach outside the `rows` rows of the operands), whether a pair has
+// each of these rows, and the two tensor maps of the rows, copies of the whole
+// operands' maps with another base address and row extent.
+//
+// A row inside the range that no pair has (its pair was dropped after the sort)
+// must add nothing, whatever dY holds there and scratch was before.  Where an
+// expert has such rows its dY map points to the copy `a_patched`, in which
+// wgrad_patch_kernel makes them zeros, as it does in X.
+constexpr int MAPS_THREADS = 256;
 struct WgradMapsParams {
   CUtensorMap map_a, map_b;
   const int* offsets;
   const uint8_t* a;
-  const uint8_t* b;
+  uint8_t* a_patched;      // may be a itself
+  uint8_t* b;
   long long a_row_bytes, b_row_bytes;
+  const uint8_t* reached;  // [rows] 1: a pair has the row; null: all of them count
   CUtensorMap* maps;
-  int2* ranges;
+  int4* ranges;            // {first row, rows, some of them without a pair, 0} of each expert
   int rows;
 };
-__global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ WgradMapsParams P) {
+__global__ void __launch_bounds__(MAPS_THREADS) wgrad_maps_kernel(const __grid_constant__ WgradMapsParams P) {
   __shared__ alignas(128) CUtensorMap sm[2];
   const int e = blockIdx.x, lane = threadIdx.x;
+  griddep_launch_dependents();
+  griddep_wait();  // the rows' pairs are being marked
   const int lo = min(max(P.offsets[e], 0), P.rows);
   const int n = max(min(P.offsets[e + 1], P.rows) - lo, 0);
+  bool hole = false;
+  if (P.reached && n > 0) {
+    // four rows' marks a word; those of rows outside the range count as set
+    const uint32_t* marks = reinterpret_cast<const uint32_t*>(P.reached);
+    const long long end = static_cast<long long>(lo) + n;
+    for (long long w = lo / 4 + static_cast<int>(threadIdx.x); 4 * w < end; w += MAPS_THREADS) {
+      uint32_t m = marks[w];
+      if (4 * w < lo) m |= (1u << (8 * (lo - static_cast<int>(4 * w)))) - 1u;
+      if (4 * w + 4 > end) m |= 0xFFFFFFFFu << (8 * static_cast<int>(end - 4 * w));
+      hole |= (m & 0x01010101u) != 0x01010101u;
+    }
+  }
+  hole = __syncthreads_or(hole) != 0;
+  if (threadIdx.x >= 32) return;
   const uint32_t* src_a = reinterpret_cast<const uint32_t*>(&P.map_a);
   const uint32_t* src_b = reinterpret_cast<const uint32_t*>(&P.map_b);
   reinterpret_cast<uint32_t*>(&sm[0])[lane] = src_a[lane];
   reinterpret_cast<uint32_t*>(&sm[1])[lane] = src_b[lane];
   __syncwarp();
   if (lane == 0) {
-    P.ranges[e] = make_int2(lo, n);
-    const uint64_t base[2] = {reinterpret_cast<uint64_t>(P.a) + static_cast<uint64_t>(lo) * P.a_row_bytes,
+    P.ranges[e] = make_int4(lo, n, hole ? 1 : 0, 0);
+    const uint64_t base[2] = {reinterpret_cast<uint64_t>(hole ? P.a_patched : P.a) + static_cast<uint64_t>(lo) * P.a_row_bytes,
                               reinterpret_cast<uint64_t>(P.b) + static_cast<uint64_t>(lo) * P.b_row_bytes};
     if (n > 0) {  // an expert without rows is never loaded; its maps stay whole (a zero extent is no map)
 #pragma unroll
@@ -125,6 +149,39 @@ __global__ void __launch_bounds__(32) wgrad_maps_kernel(const __grid_constant__ 
                      reinterpret_cast<uint64_t>(P.maps + 2 * e + i)),
                  "r"(smem_u32(&sm[i]))
                  : "memory");
+}
+// The rows of experts that have some without a pair: dY's to a_patched, and those
+// without a pair as zeros there and in X.  A warp takes a row.  (No expert has any
+// when the plan is as the sort made it; then this is an empty launch.)
+__global__ void __launch_bounds__(MAPS_THREADS) wgrad_patch_kernel(const WgradMapsParams P, int experts) {
+  __shared__ int4 range[MAPS_THREADS];
+  griddep_launch_dependents();  // the product may set itself up
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * (MAPS_THREADS / 32);
+  const long long first = (long long)blockIdx.x * (MAPS_THREADS / 32) + (threadIdx.x >> 5);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int e0 = 0; e0 < experts; e0 += MAPS_THREADS) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    const int4 mine = e < experts ? P.ranges[e] : make_int4(0, 0, 0, 0);
+    range[threadIdx.x] = mine;
+    const bool some = __syncthreads_or(mine.z) != 0;
+    for (int i = 0; some && i < min(MAPS_THREADS, experts - e0); ++i) {
+      if (!range[i].z) continue;
+      for (long long k = first; k < range[i].y; k += warps) {
+        const long long row = range[i].x + k;
+        const bool kept = P.reached[row] != 0;
+        const uint4* src = reinterpret_cast<const uint4*>(P.a + row * P.a_row_bytes);
+        uint4* dst = reinterpret_cast<uint4*>(P.a_patched + row * P.a_row_bytes);
+        uint4* x = reinterpret_cast<uint4*>(P.b + row * P.b_row_bytes);
+        if (!kept || src != dst)
+          for (long long c = lane; c < P.a_row_bytes / 16; c += 32) dst[c] = kept ? src[c] : zero;
+        if (!kept)
+          for (long long c = lane; c < P.b_row_bytes / 16; c += 32) x[c] = zero;
+      }
+    }
+    __syncthreads();  // before the next experts' ranges
+  }
 }
 
 // ------------------------------------------------------------------- tiles

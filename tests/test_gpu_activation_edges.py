@@ -1,9 +1,11 @@
 """GPU tests of the activation operators where their results are decided exactly:
-long sums of one sign."""
+long sums of one sign, and pairs dropped after the sort."""
+import numpy as np
 import pytest
 import torch
 
 import matrix_orthogonalising_optimizer_step_b200 as mc
+from oracle import activations as oa
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -16,8 +18,23 @@ def gen(seed):
     return g
 
 
+def draw(seed, *shape, std=1.0, dtype=BF):
+    return (torch.randn(*shape, generator=gen(seed), device=DEV) * std).to(dtype)
+
+
+def n64(t):
+    return t.detach().to("cpu", torch.float64).numpy()
+
+
 def ok():
     assert mc.device_status() == mc.MC_OK, mc.last_error()
+
+
+def stored(a):
+    """(values, scale bytes) of an Act8, as the oracle reads them."""
+    D = a.shape[-1]
+    s = a.scale.cpu().numpy()
+    return oa.act8_values(a.q.cpu().numpy(), s, D, a.fmt), s[:, :-(-D // 32)]
 
 
 # ------------------------------------------------------- bf16 and fp32 sums
@@ -72,3 +89,71 @@ def test_long_sums_of_one_weights_whole_tiles(dtype):
     want = dy.double().t() @ (x.q[:, some].double() * 2.0 ** -7)
     check_long_sum(g[:, some], want)
     ok()
+
+
+# ------------------------------------------------------------ dropped pairs
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,K,E,M,N", [(300, 2, 4, 64, 96), (130, 8, 9, 40, 33), (1000, 1, 3, 264, 520), (70, 3, 2, 33, 64), (2000, 4, 5, 128, 2056)])
+def test_experts_gradient_without_pairs_dropped_after_the_sort(T, K, E, M, N, dtype):
+    """Positions set outside the rows after the sort (an expert over its capacity): those
+    pairs add nothing, whatever their rows of dy and the scratch hold."""
+    g = gen(T)
+    plan = mc.expert_sort(torch.randint(-1, E, (T, K), generator=g, device=DEV), E)
+    off = plan.offsets.tolist()
+    gone = torch.rand(T, K, generator=g, device=DEV) < 0.2
+    gone |= (plan.position >= off[1]) & (plan.position < off[2])            # expert 1 loses every pair
+    lost = plan.position[gone & (plan.position >= 0)].long()
+    away = torch.tensor([-1, T * K, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=DEV)[torch.randint(0, 4, (T, K), generator=g, device=DEV)]
+    kept = plan._replace(position=torch.where(gone, away, plan.position))
+    dy = draw(T + 1, T * K, M)
+    dy[lost] = float("nan")
+    x = mc.act8_pack(draw(T + 2, T, N), "e4m3")
+    x64, _ = stored(x)
+    src, reached = plan.source.cpu().numpy().clip(0) // K, np.zeros(T * K, bool)
+    pos = kept.position.cpu().numpy().reshape(-1)
+    reached[pos[(pos >= 0) & (pos < T * K)]] = True
+    need = mc.load_library().mc_expert_weight_grad_workspace_size(T * K, E, M, N)
+    base = draw(T + 3, E, M, N, dtype=F32)
+    for accumulate in ((False, True) if dtype == F32 else (False,)):
+        ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)        # bf16 NaN
+        out = base.clone() if accumulate else None
+        got = n64(mc.expert_weight_grad(dy, x, kept, gather=True, dtype=dtype, out=out, accumulate=accumulate, workspace=ws))
+        ok()
+        for e in range(E):
+            r = np.arange(off[e], off[e + 1])
+            r = r[reached[r]]
+            a, b = n64(dy)[r], x64[src[r]]
+            want, size = a.T @ b, np.abs(a).T @ np.abs(b)
+            bound = (len(r) + 64) * 2.0 ** -23 * size
+            if accumulate:
+                want = want + n64(base[e])
+                bound = bound + 2.0 ** -23 * (np.abs(want) + size)
+            if dtype == BF:
+                bound = bound + 2.0 ** -8 * np.abs(want)
+            assert np.all(np.abs(got[e] - want) <= bound + 2.0 ** -134), e
+        assert accumulate or (got[1] == 0).all()
+
+
+def test_a_captured_experts_gradient_follows_the_positions():
+    """Replayed with pairs dropped, with others dropped, and with all of them back."""
+    T, K, E, M, N = 500, 2, 3, 64, 72
+    plan = mc.expert_sort(torch.randint(0, E, (T, K), generator=gen(1), device=DEV), E)
+    dy, x = draw(2, T * K, M), mc.act8_pack(draw(3, T, N), "int8")
+    whole = plan.position.clone()
+    want = mc.expert_weight_grad(dy, x, plan, gather=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = mc.expert_weight_grad(dy, x, plan, gather=True)
+    for seed in (4, 5, None):
+        gone = torch.rand(T, K, generator=gen(seed), device=DEV) < 0.3 if seed else torch.zeros_like(whole, dtype=torch.bool)
+        plan.position.copy_(torch.where(gone, torch.full_like(whole, -1), whole))
+        g.replay()
+        torch.cuda.synchronize()
+        if seed is None:
+            assert torch.equal(got, want)
+            continue
+        zeroed = dy.clone()
+        zeroed[whole[gone].long()] = 0                                      # whole plan, those rows as zeros: the same sums
+        assert torch.equal(got, mc.expert_weight_grad(zeroed, x, plan._replace(position=whole), gather=True))
+    ok()
+    del g

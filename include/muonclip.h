@@ -512,9 +512,10 @@ int mc_act8_unpack(const mc_act8* a, void* out, int out_dtype, void* stream);
  * mc_rms_norm -- root-mean-square norm with the residual's addition:
  *   h = x + residual, rounded to dtype and stored in h_out (residual and h_out
  *       both NULL: h = x);  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * w
- * in fp32 from the stored h.  y goes to y_out (bf16) or, unrounded, to the 8-bit
- * y8: exactly one of them is given.  h_out may be x or residual itself; nothing
- * else may overlap.
+ * from the stored h, its squares in fp32 (finite for |h| up to 1.8e19).  y goes to
+ * y_out (bf16) or, unrounded, to the 8-bit y8: exactly one of them is given.  What
+ * lies on the border of two codes or scales (within 2^-40) is taken as the border.
+ * h_out may be x or residual itself; nothing else may overlap.
  * x, residual, h_out  device, rows x cols, dtype (MC_F32 or MC_BF16)
  * w                   device, cols, w_dtype
  * rstd_out            device fp32 [rows]

@@ -663,7 +663,8 @@ MC_API int mc_rms_norm(const void* x, const void* residual, const void* w, int d
     a.D = static_cast<int>(cols);
     a.w_f32 = w_dtype == MC_F32 ? 1 : 0;
     a.eps = eps;
-    a.inv_d = 1.0 / static_cast<double>(cols);
+    a.d = static_cast<double>(cols);
+    a.inv_d = 1.0 / a.d;
     with_fmt(y8 ? y8->fmt : -1, [&](auto f) {
       with_group(cols, [&](auto g) {
         constexpr int F = decltype(f)::value;

@@ -47,20 +47,52 @@ __device__ __forceinline__ double rsqrt64(double m) {
   return 1.0 / sqrt(m);
 }
 
-// x * r * w for an 8-bit output, as fp32 rounded to odd: r is given as
-// r_hi + r_lo, the product is kept to about 2^-46, cut toward zero and given an
-// odd last bit.  A rounding to 8 bits of it is then the rounding of the product
-// itself: a value just beside the middle of two codes never looks like the
-// middle (one exactly there, which takes an r of few bits, goes away from zero).
-// Infinities become NaN, which stands for the same in 8 bits.
-__device__ __forceinline__ float scaled_to_odd(float x, float w, float r_hi, float r_lo) {
-  const float t_hi = r_hi * w;
-  const float t_lo = fmaf(r_lo, w, fmaf(r_hi, w, -t_hi));
-  return __int_as_float(__float_as_int(__fmaf_rz(x, t_hi, x * t_lo)) | 1);
-}
-// The same where x * w is exact in fp32 (two bf16 numbers).
-__device__ __forceinline__ float scaled_to_odd(float xw, float r_hi, float r_lo) {
-  return __int_as_float(__float_as_int(__fmaf_rz(xw, r_hi, xw * r_lo)) | 1);
+// v * r * w of eight values for an 8-bit output, r given as r_hi + r_lo: fp32 numbers
+// that round to 8 bits as the products themselves do.  The products are known to
+// about 2^-43 and rounded to the nearest fp32 number, which lies on the same side
+// as the product of everything that decides a code or a scale, the middle of two
+// codes and the largest value of a scale: those have at most 8 significant bits.  Only
+// a result that has as few may have been rounded to such a border; it goes
+// back to the side that the product is on, one step off, unless the product
+// is within 2^-40 of it: that is the border (a tie, to even; the largest value, in its scale).
+// BF16: v and w are bf16 numbers, whose product is exact in fp32.
+template <bool BF16>
+__device__ __forceinline__ void scaled_for_codes(float (&v)[8], const float (&w)[8], float r_hi, float r_lo) {
+  auto factors = [&](int i, float& x, float& t_hi, float& t_lo) {
+    if constexpr (BF16) {
+      x = v[i] * w[i];
+      t_hi = r_hi;
+      t_lo = r_lo;
+    } else {
+      x = v[i];
+      t_hi = r_hi * w[i];
+      t_lo = fmaf(r_lo, w[i], fmaf(r_hi, w[i], -t_hi));
+    }
+  };
+  float p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x, t_hi, t_lo;
+    factors(i, x, t_hi, t_lo);
+    p[i] = fmaf(x, t_hi, x * t_lo);
+  }
+  // the least lower half of the eight words
+  auto word = [&](int i) { return __float_as_uint(p[i]); };
+  const uint32_t least = __vminu2(__vimin3_u16x2(__vimin3_u16x2(word(0), word(1), word(2)), word(3), word(4)),
+                                  __vimin3_u16x2(word(5), word(6), word(7)));
+  if ((least & 0xFFFFu) == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (__float_as_uint(p[i]) & 0xFFFFu) continue;
+      float x, t_hi, t_lo;
+      factors(i, x, t_hi, t_lo);
+      const float rest = fmaf(x, t_hi, -p[i]) + x * t_lo;
+      if (fabsf(rest) > 0x1p-40f * fabsf(p[i]))
+        p[i] = __int_as_float(__float_as_int(p[i]) + ((rest > 0.f) == (p[i] > 0.f) ? 1 : -1));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = p[i];
 }
 
 // The norm's weight of one fragment (bf16 or fp32), 0 past D.
@@ -90,14 +122,16 @@ struct NormFwdArgs {
   long long rows, q_ld, s_ld;
   int D, w_f32;
   float eps;
-  double inv_d;        // 1 / D
+  double d, inv_d;     // D and 1 / D
 };
 
 // The sum of squares is kept in 64 bits beyond each fragment's eight terms: its
 // error would move every value of the row the same way.  (Every square in 64
 // bits: 115 us for 16384 x 4096 bf16 rows, bound by the conversions.)
+// Four blocks an SM for bf16 rows: left to itself the compiler takes a few registers
+// more than that allows (16384 x 4096: 88 us, 8192 x 4095: 111 us; so 79 and 85).
 template <typename T, int FMT, int G, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<T> a) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 && sizeof(T) == 2 ? 4 : 1) rms_norm_kernel(const NormFwdArgs<T> a) {
   __shared__ double buf[32];
   griddep_launch_dependents();
   // blockDim: {32 * warps of a row, rows}
@@ -132,7 +166,10 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<
   }
   sum = row_sum(sum, wpr, threadIdx.y * wpr, wr, buf);
   if (!live) return;
-  const double r64 = rsqrt64(fma(sum, a.inv_d, static_cast<double>(a.eps)));
+  // sum / D: exact where it is a number of 53 bits (an infinite sum stays so)
+  const double near = sum * a.inv_d;
+  const double mean = fma(fma(-near, a.d, sum), a.inv_d, near);
+  const double r64 = rsqrt64((mean == mean ? mean : near) + static_cast<double>(a.eps));
   const float rstd = static_cast<float>(r64);
   const float r_lo = static_cast<float>(r64 - static_cast<double>(rstd));
   if (wr == 0 && lane == 0) a.rstd[row] = rstd;
@@ -150,11 +187,9 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const NormFwdArgs<
       store_frag<G>(a.y + base, c0, lane, a.D, v);
     } else {
       if (sizeof(T) == 2 && !a.w_f32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i] * w[i], rstd, r_lo);
+        scaled_for_codes<true>(v, w, rstd, r_lo);
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = scaled_to_odd(v[i], w[i], rstd, r_lo);
+        scaled_for_codes<false>(v, w, rstd, r_lo);
       }
       store_frag8<FMT, G>(a.q + row * a.q_ld, a.s + row * a.s_ld, c0, lane, a.D, v);
     }

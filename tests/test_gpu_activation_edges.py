@@ -1,5 +1,6 @@
 """GPU tests of the activation operators where their results are decided exactly:
-long sums of one sign, and pairs dropped after the sort."""
+8-bit outputs of the norm at the borders of scales and codes, long sums of one
+sign, and pairs dropped after the sort."""
 import numpy as np
 import pytest
 import torch
@@ -157,3 +158,64 @@ def test_a_captured_experts_gradient_follows_the_positions():
         assert torch.equal(got, mc.expert_weight_grad(zeroed, x, plan._replace(position=whole), gather=True))
     ok()
     del g
+
+
+# ------------------------------------------------- the norm's 8-bit borders
+BORDERS = {"int8": [127 / 64, 126.5 / 64, 125.5 / 64, 1.0, 0.5 / 64, 1.5 / 64, 64.5 / 64, 3.5 / 64],
+           "e4m3": [1.75, 1.6875, 1.0625, 1.1875, 17 / 1024, 19 / 1024, 2.0 ** -17, 1.5 * 2.0 ** -17, 1.0]}
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [8, 64, 1000, 4096, 66, 1594, 67, 1789, 8200])
+def test_norm_at_the_borders_of_scales_and_codes(D, dtype, fmt):
+    """Rows whose y = h rstd w is known exactly: +-c everywhere gives +-w (eps = 0), +-1
+    with eps = 3 gives +-w / 2.  The weights stand at the largest value of a
+    scale and in the middle of two codes: the least scale, and ties to even."""
+    w = torch.tensor(BORDERS[fmt], device=DEV).repeat(D // len(BORDERS[fmt]) + 1)[:D]
+    w = torch.where(torch.rand(D, generator=gen(D), device=DEV) < 0.5, -w, w)
+    sizes = torch.tensor([1.0, 2.0 ** -3, 2.0 ** 7, 3.0, 5.0, 0.109375, 113.0, 1.3125], device=DEV)
+    sign = torch.where(torch.rand(sizes.numel(), D, generator=gen(D + 1), device=DEV) < 0.5, -1.0, 1.0)
+    for wdtype in (BF, F32):
+        w_ = w.to(wdtype)
+        for x, eps, factor in (((sign * sizes[:, None]).to(dtype), 0.0, 1.0), (sign.to(dtype), 3.0, 0.5)):
+            y = mc.rms_norm(x, w_, eps=eps, fmt=fmt).y
+            ok()
+            got, scale = stored(y)
+            want, want_scale = oa.act8(n64(sign) * n64(w)[None, :] * factor, fmt)
+            assert np.array_equal(scale, want_scale), (wdtype, eps)
+            assert np.array_equal(got, want), (wdtype, eps)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [256, 258, 1024])
+def test_norm_of_one_value_a_row(D, fmt):
+    """c alone in a row: y = sqrt(D) w there (a power of two times w where D is one of four)."""
+    x = torch.zeros(64, D, dtype=BF, device=DEV)
+    col = torch.randint(0, D, (64,), generator=gen(D), device=DEV)
+    c = draw(D + 1, 64)
+    x[torch.arange(64, device=DEV), col] = c
+    w = torch.full((D,), oa.TOP[fmt], dtype=BF, device=DEV)
+    got, scale = stored(mc.rms_norm(x, w, eps=0.0, fmt=fmt).y)
+    y = np.zeros((64, D))
+    y[np.arange(64), col.cpu().numpy()] = np.sign(n64(c)) * np.sqrt(D) * oa.TOP[fmt]
+    want, want_scale = oa.act8(y, fmt)
+    assert np.array_equal(got, want) and np.array_equal(scale, want_scale)
+    ok()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,wdtype", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("T,D", [(600, 4096), (700, 1594), (700, 1789)])
+def test_norm_rounds_the_product_itself(T, D, dtype, wdtype, fmt):
+    """Every code is that of a product within 2^-21 of the formula's: the sums of eight
+    squares round eight times at most, 2^-24 each, and the root halves that; everything
+    behind is kept to more bits."""
+    x, w = draw(T, T, D, std=2.0, dtype=dtype), (1 + 0.2 * draw(D, D, dtype=F32)).to(wdtype)
+    y, _ = oa.rms_norm(n64(x), n64(w), 1e-6)
+    got, scale = stored(mc.rms_norm(x, w, fmt=fmt).y)
+    ok()
+    lo, lo_scale = oa.act8(y * (1 - 2.0 ** -21), fmt)
+    hi, hi_scale = oa.act8(y * (1 + 2.0 ** -21), fmt)
+    assert ((scale == lo_scale) | (scale == hi_scale)).all()
+    assert ((got == lo) | (got == hi)).all(), int(((got != lo) & (got != hi)).sum())

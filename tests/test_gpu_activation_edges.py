@@ -1,6 +1,6 @@
 """GPU tests of the activation operators where their results are decided exactly:
 8-bit outputs of the norm at the borders of scales and codes, long sums of one
-sign, and pairs dropped after the sort."""
+sign, pairs dropped after the sort, every path of the sort, and captured packing."""
 import numpy as np
 import pytest
 import torch
@@ -219,3 +219,44 @@ def test_norm_rounds_the_product_itself(T, D, dtype, wdtype, fmt):
     hi, hi_scale = oa.act8(y * (1 + 2.0 ** -21), fmt)
     assert ((scale == lo_scale) | (scale == hi_scale)).all()
     assert ((got == lo) | (got == hi)).all(), int(((got != lo) & (got != hi)).sum())
+
+
+# ----------------------------------------------------------------- the sort
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("T,K,E", [(2048, 1, 64), (2049, 1, 64), (4096, 8, 64), (32769, 1, 60), (8192, 8, 64), (8192, 8, 1024), (16384, 8, 3),
+                                   (131073, 1, 64)])
+def test_sort_by_every_path(T, K, E, dtype):
+    """One block; the cluster launch up to 32,768 pairs; counting and placing launches
+    up to 131,072; with a scan between them beyond that."""
+    idx = torch.randint(0, E, (T, K), generator=gen(T + E), device=DEV)
+    idx = torch.where(torch.rand(T, K, generator=gen(T), device=DEV) < 0.05, torch.full_like(idx, -1), idx).to(dtype)
+    idx[:3] = E                                                             # dropped too
+    plan = mc.expert_sort(idx, E)
+    ok()
+    offsets, source, position = oa.expert_sort(idx.cpu().numpy(), E)
+    assert np.array_equal(plan.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(plan.source.cpu().numpy(), source)
+    assert np.array_equal(plan.position.cpu().numpy(), position)
+
+
+# ---------------------------------------------------------- captured packing
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [520, 514, 521])
+def test_captured_pack_writes_every_code_and_scale(D, fmt):
+    x = draw(D, 300, D)
+    out = mc.act8_pack(x, fmt)
+    want, scale = oa.act8(n64(x), fmt)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mc.act8_pack(x, fmt, out=out)
+        back = mc.act8_unpack(out)
+    for _ in range(2):
+        out.q.zero_()
+        out.scale.zero_()
+        back.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got, got_scale = stored(out)
+        assert np.array_equal(got, want) and np.array_equal(got_scale, scale) and np.array_equal(n64(back), want)
+    ok()
+    del g

@@ -8,6 +8,10 @@ They make what the step takes: the layer inputs x of ``qk_max_logit`` and
 Results are allocated with torch on the stream that the call runs on unless
 ``out`` is given; so is scratch, unless ``workspace`` is.  All calls can be
 captured into a CUDA graph.
+
+No call records an autograd graph: results never require gradients, whatever
+the inputs do.  Backward passes are calls of their own, made by the training loop or
+from the ``backward`` of a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 

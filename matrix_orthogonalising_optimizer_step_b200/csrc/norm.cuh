@@ -11,9 +11,9 @@
 // shared memory (backward) between its sum and its output, and written once.
 // `wpr` warps share a row (a warp holds 256 columns per fragment, NV fragments),
 // so a block of 8 warps takes 8 / wpr rows; sums are trees of a fixed order.
-// Measured on 16384 x 4096 bf16 rows: forward with residual and e4m3 output 80 us
-// (472 MB, 5.9 TB/s of the 6.55 a copy reaches here), backward 95 us (537 MB, 5.7
-// TB/s) and under 8 us for the sum of dw's parts.
+// Measured on 16384 x 4096 bf16 rows: forward with residual and e4m3 output 79 us
+// (472 MB, 6.0 TB/s of the 6.55 a copy reaches here), to bf16 84 us (537 MB, 6.4 TB/s),
+// backward 94 us (537 MB, 5.7 TB/s) with under 8 us for the sum of dw's parts in it.
 #pragma once
 
 #include "act8.cuh"
